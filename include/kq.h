@@ -282,6 +282,98 @@ int kq_quantize_weight_tiled(const uint16_t* w, int64_t N, int64_t d, const floa
 int kq_scales_to_tiled(const uint8_t* scales, int64_t rows, int64_t K, uint8_t* tiled,
                        void* stream);
 
+/* ---- MXFP4 K/V cache and attention over it -------------------------------
+ * Keys and values of an attention layer kept as the quantizer writes MXFP4
+ * (E2M1 codes, an E8M0 scale byte per 32 channels, the floor rule above): the
+ * states of a text encoder, which stay the same over the steps of a denoiser,
+ * or the growing context of a causal model.  Rows are quantized as they are;
+ * a transform T of a head's channels belongs in the projections in front
+ * (q T^-T and k T leave q k^T unchanged).
+ *
+ * The cache is a pool of pages.  A page holds page_size positions of every
+ * K/V head:
+ *   codes  [pages][heads][page_size][Dp / 2]   (element 2i low nibble)
+ *   scales [pages][heads][page_size][Dp / 32]
+ * with Dp = head_dim rounded up to a multiple of 32; the channels past
+ * head_dim are zeros.  Where head_dim is a multiple of 32, kq_dequantize
+ * decodes a cache array as it stands.  block_table is int32 [batch][table_pages]:
+ * position p of sequence b is slot p mod page_size of page
+ * block_table[b][p / page_size].  Sequences may share pages that are only
+ * read (a prompt's prefix, the empty prompt of a guided sampler).
+ *   page_size: a power of two from 16 to 65536; pages below 2^31;
+ *   heads: 1 to 65535; head_dim: a multiple of 8 from 8 to 128;
+ *   batch at most 65535; table_pages * page_size below 2^31.
+ * The four arrays are 16-byte aligned, block_table 4-byte aligned.  Values of
+ * magnitude 2^60 and above, NaN and Inf are outside the contract, as are
+ * scale bytes the quantizer does not write for the others.
+ * A row whose position is negative, lies past its table or on a page outside
+ * [0, pages) is left out, and KQ_DEVERR_CACHE_INDEX is set in the device error
+ * word; no other row is affected. */
+typedef struct {
+    uint8_t* k_codes;
+    uint8_t* k_scales;
+    uint8_t* v_codes;
+    uint8_t* v_scales;
+    int64_t pages;
+    int64_t page_size;
+    int64_t heads;
+    int64_t head_dim;
+} kq_cache;
+
+/* Quantizes rows into the cache: row t < lens[b] of sequence b goes to
+ * position start[b] + t, for K and V alike.
+ *   k, v: bf16, element (b, t, h, c) at b * sb + t * st + h * sh + c; pointers
+ *   16-byte aligned, strides non-negative multiples of 8 (slices of one
+ *   projection's output pass as they are).
+ *   start, lens: int32 [batch] device arrays; NULL: 0, and all `tokens` rows.
+ *   lens[b] above `tokens` counts as `tokens`; rows at or past it, and slots no
+ *   row goes to, are left as they were.
+ * Two rows of one call must not go to the same slot (two sequences writing to
+ * a shared page): that slot's contents are unspecified then. */
+int kq_cache_write(const kq_cache* cache, const int32_t* block_table, int64_t batch,
+                   int64_t table_pages, const uint16_t* k, int64_t k_sb, int64_t k_st,
+                   int64_t k_sh, const uint16_t* v, int64_t v_sb, int64_t v_st, int64_t v_sh,
+                   int64_t tokens, const int32_t* start, const int32_t* lens, void* stream);
+
+/* Reads rows back: row t < lens[b] of k and v is position start[b] + t,
+ * decoded (exactly: E2M1 times a power of two, in bf16 or float32 by dtype
+ * KQ_OUT_*); the other rows, and rows left out, are written as zeros.
+ * Strides as above, in elements of dtype and multiples of 16 bytes; the
+ * elements of k and v must not overlap. */
+int kq_cache_read(const kq_cache* cache, const int32_t* block_table, int64_t batch,
+                  int64_t table_pages, int64_t tokens, const int32_t* start, const int32_t* lens,
+                  void* k, int64_t k_sb, int64_t k_st, int64_t k_sh, void* v, int64_t v_sb,
+                  int64_t v_st, int64_t v_sh, int dtype, void* stream);
+
+/* Attention of M queries a sequence over its len[b] = min(lens[b], max_len)
+ * cached positions, of another length than M:
+ *   out[b][m][h] = sum_p softmax_p(scale q[b][m][h] . K[p]) V[p]
+ * over p < len[b], with causal != 0 also p <= len[b] - M + m (the queries are
+ * the last M positions); head h reads K/V head h / (heads / kv heads).  A row
+ * that sees no position has out = 0 and lse = -inf.
+ *   q: bf16, element (b, m, h, c) at b * q_sb + m * q_sm + h * q_sh + c;
+ *   out: bf16 with strides o_*; pointers 16-byte aligned, strides non-negative
+ *   multiples of 8.  out must not overlap q.
+ *   lse: float32 [batch][heads][M], the natural log-sum-exp of the scaled
+ *   scores, or NULL.
+ *   max_len: a bound on lens, at most table_pages * page_size; the work is cut
+ *   by it, so a tight one is faster.
+ *   workspace: kq_attention_workspace_bytes(...) bytes, 256-byte aligned (NULL
+ *   where that is 0); its contents before and after do not matter.  Calls that
+ *   overlap on the GPU need their own.
+ * Products of bf16 with float32 sums; maximum, sum and output accumulator are
+ * float32; the softmax weights are rounded to bf16 for the second product.
+ * Positions on pages outside the pool are not seen (KQ_DEVERR_CACHE_INDEX).
+ * The result does not depend on the order in which blocks run. */
+size_t kq_attention_workspace_bytes(int64_t batch, int64_t M, int64_t heads, int64_t kv_heads,
+                                    int64_t head_dim, int64_t max_len);
+int kq_attention_mxfp4(const uint16_t* q, int64_t q_sb, int64_t q_sm, int64_t q_sh,
+                       int64_t batch, int64_t M, int64_t heads, const kq_cache* cache,
+                       const int32_t* block_table, int64_t table_pages, const int32_t* lens,
+                       int64_t max_len, float scale, int causal, uint16_t* out, int64_t o_sb,
+                       int64_t o_sm, int64_t o_sh, float* lse, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 /* x = y T^-1 in float32 with T^-1 = diag(G1^-1 (x) ... (x) G5^-1) (review,
  * axiom ledger: the inverse of a Kronecker product factorizes), computed in
  * double and rounded once as kq_transform is.  y: [M][d] float32, x: [M][d]
@@ -358,15 +450,17 @@ const char* kq_status_string(int status);
 int kq_last_cuda_error(void);
 
 /* Synchronises the current device, then reads and clears the library's
- * device-side error word: 0 if every bounded in-kernel wait finished,
- * otherwise a bit mask of the waits that gave up (kernels that give up stop
- * early and leave their outputs incomplete).  Returns KQ_OK or KQ_ERR_CUDA. */
+ * device-side error word: 0 if every bounded in-kernel wait finished and
+ * every cache position had its page, otherwise a bit mask of what did not
+ * (kernels whose wait gives up stop early and leave their outputs incomplete).
+ * Returns KQ_OK or KQ_ERR_CUDA. */
 int kq_device_status(int* flags);
 
 /* Device-side error word bits (kq_device_status). */
 #define KQ_DEVERR_CONSUMER_WAIT 1  /* a consumer gave up waiting for its data */
 #define KQ_DEVERR_PRODUCER_WAIT 2  /* a producer gave up waiting for a free stage */
 #define KQ_DEVERR_SELFTEST 4       /* set by kq_selftest_wait_timeout */
+#define KQ_DEVERR_CACHE_INDEX 8    /* a cache position without a page in the pool */
 
 /* Self-test of the bounded waits: launches one tiny kernel that waits (at
  * most 64 polls of about 1 us) on a barrier nothing completes, gives up and

@@ -57,6 +57,14 @@ SIGNATURES = {
     "kq_quantize_adaln": [_p, _i64, _i64, _p, _p, _i64, ctypes.c_float, _p, _p, _p, _p],
     "kq_quantize_adaln_tiled": [_p, _i64, _i64, _p, _p, _i64, ctypes.c_float, _p, _p, _p, _p],
     "kq_transform_adaln": [_p, _i64, _i64, _p, _p, _i64, ctypes.c_float, _p, _p, _p],
+    "kq_cache_write": [_p, _p, _i64, _i64, _p, _i64, _i64, _i64, _p, _i64, _i64, _i64, _i64, _p, _p,
+                       _p],
+    "kq_cache_read": [_p, _p, _i64, _i64, _i64, _p, _p, _p, _i64, _i64, _i64, _p, _i64, _i64, _i64,
+                      _int, _p],
+    "kq_attention_workspace_bytes": [_i64, _i64, _i64, _i64, _i64, _i64],
+    "kq_attention_mxfp4": [_p, _i64, _i64, _i64, _i64, _i64, _i64, _p, _p, _i64, _p, _i64,
+                           ctypes.c_float, _int, _p, _i64, _i64, _i64, _p, _p, ctypes.c_size_t,
+                           _p],
     "kq_inverse_transform": [_p, _i64, _i64, _p, _p, _p],
     "kq_dequantize": [_p, _p, _i64, _i64, _p, _p],
     "kq_quantize_host": [_p, _i64, _i64, _p, _p, _p, _p, ctypes.c_size_t, _p],
@@ -72,6 +80,7 @@ _RESTYPE = {"kq_status_string": ctypes.c_char_p,
             "kq_quantize_host_workspace_bytes": ctypes.c_size_t,
             "kq_transform_params_grad_workspace_bytes": ctypes.c_size_t,
             "kq_residual_workspace_bytes": ctypes.c_size_t,
+            "kq_attention_workspace_bytes": ctypes.c_size_t,
             "kq_scales_tiled_bytes": ctypes.c_size_t,
             "kq_scales16_tiled_bytes": ctypes.c_size_t}
 
@@ -578,6 +587,221 @@ def gemm_mxfp4_tiled(qa: torch.Tensor, sa_tiled: torch.Tensor, qb: torch.Tensor,
                                    sb_tiled.data_ptr(), M, N, K, out.data_ptr(), code,
                                    _stream(qa.device))
     _check("kq_gemm_mxfp4_tiled", st)
+    return out
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k_codes", _p), ("k_scales", _p), ("v_codes", _p), ("v_scales", _p),
+                ("pages", _i64), ("page_size", _i64), ("heads", _i64), ("head_dim", _i64)]
+
+
+class KVCache:
+    """A pool of MXFP4 K/V pages: codes uint8 [pages, heads, page_size, Dp/2]
+    and scale bytes uint8 [pages, heads, page_size, Dp/32] for K and for V, Dp =
+    head_dim rounded up to 32.  Holds the caller's tensors; ``cache_alloc``
+    makes new ones."""
+
+    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "pages", "page_size", "heads",
+                 "head_dim", "device", "_c", "_ptr")
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                 v_scales: torch.Tensor, head_dim: int):
+        head_dim = int(head_dim)
+        if head_dim < 8 or head_dim > 128 or head_dim % 8 != 0:
+            raise ValueError("head_dim must be a multiple of 8 from 8 to 128")
+        nb = -(-head_dim // 32)
+        for t, n in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"),
+                     (v_scales, "v_scales")):
+            _dev_tensor(t, torch.uint8, n)
+            if t.device != k_codes.device:
+                raise ValueError("the cache's tensors must be on one device")
+            if t.dim() != 4 or t.shape[:3] != k_codes.shape[:3] or \
+                    t.shape[3] != (16 * nb if n.endswith("codes") else nb):
+                raise ValueError(f"{n} must be [pages, heads, page_size, "
+                                 f"{'Dp/2' if n.endswith('codes') else 'Dp/32'}]")
+        pages, heads, page_size = k_codes.shape[:3]
+        if page_size < 16 or page_size > 65536 or page_size & (page_size - 1):
+            raise ValueError("page_size must be a power of two from 16 to 65536")
+        if pages < 1 or heads < 1:
+            raise ValueError("the cache needs a page and a head")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = \
+            k_codes, k_scales, v_codes, v_scales
+        self.pages, self.page_size, self.heads, self.head_dim = pages, page_size, heads, head_dim
+        self.device = k_codes.device
+        self._c = _CacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                               v_scales.data_ptr(), pages, page_size, heads, head_dim)
+        self._ptr = ctypes.addressof(self._c)
+
+
+def cache_alloc(pages: int, page_size: int, heads: int, head_dim: int, device="cuda") -> KVCache:
+    """A KVCache of zeroed pages."""
+    nb = -(-int(head_dim) // 32)
+
+    def make(n):
+        return torch.zeros((pages, heads, page_size, n), dtype=torch.uint8, device=device)
+    return KVCache(make(16 * nb), make(nb), make(16 * nb), make(nb), head_dim)
+
+
+def _call(name: str, device: torch.device, *args):
+    """Calls an entry point on the current stream of ``device``, with that
+    device current."""
+    fn = getattr(lib(), name)
+    if device.index == torch.cuda.current_device():
+        st = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(device))
+    _check(name, st)
+
+
+def _cache_index(cache: KVCache, block_table: torch.Tensor, batch: int, per_seq):
+    """Checks a block table and int32 [batch] arrays on the cache's device."""
+    _dev_tensor(block_table, torch.int32, "block_table")
+    if block_table.dim() != 2 or block_table.shape[0] != batch or block_table.shape[1] < 1:
+        raise ValueError("block_table must be int32 [batch, pages of a sequence]")
+    if block_table.device != cache.device:
+        raise ValueError("block_table must be on the cache's device")
+    for t, n in per_seq:
+        if t is not None:
+            _dev_tensor(t, torch.int32, n)
+            if tuple(t.shape) != (batch,) or t.device != cache.device:
+                raise ValueError(f"{n} must be int32 [batch] on the cache's device")
+
+
+def _head_rows(x: torch.Tensor, dtype, name: str, device):
+    """Checks [batch, rows, heads, head_dim] rows of unit channel stride whose
+    rows start on 16-byte boundaries; returns the strides of the first three
+    (0 for a dimension of size 1, whose stride has no meaning)."""
+    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.device != device:
+        raise ValueError(f"{name} must be on the cache's device")
+    if x.dim() != 4:
+        raise ValueError(f"{name} must be [batch, rows, heads, head_dim]")
+    strides = x.stride()
+    if strides[3] != 1 and x.shape[3] > 1:
+        raise ValueError(f"{name} must have unit stride along head_dim")
+    unit = 16 // x.element_size()
+    sb, st, sh = (s if n > 1 else 0 for s, n in zip(strides, x.shape[:3]))
+    if sb % unit or st % unit or sh % unit or x.data_ptr() % 16:
+        raise ValueError(f"every row of {name} must start on a 16-byte boundary")
+    return sb, st, sh
+
+
+def _disjoint_rows(x: torch.Tensor, name: str):
+    """An output's rows must not overlap one another."""
+    if x.is_contiguous():
+        return
+    reach = 0
+    for s, n in sorted((s, n) for s, n in zip(x.stride(), x.shape) if n > 1):
+        if s <= reach:
+            raise ValueError(f"the rows of {name} overlap")
+        reach += s * (n - 1)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def cache_write(cache: KVCache, block_table: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                start=None, lens=None) -> KVCache:
+    """Quantizes rows into the cache: row t < lens[b] (default: every row) of
+    bf16 k and v [batch, tokens, heads, head_dim] goes to position start[b] + t
+    (default: t) of sequence b, page block_table[b, position // page_size].
+    Everything else in the cache stays as it was."""
+    ks = _head_rows(k, torch.bfloat16, "k", cache.device)
+    vs = _head_rows(v, torch.bfloat16, "v", cache.device)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    B, T, H, D = k.shape
+    if H != cache.heads or D != cache.head_dim:
+        raise ValueError("k and v must have the cache's heads and head_dim")
+    _cache_index(cache, block_table, B, ((start, "start"), (lens, "lens")))
+    _call("kq_cache_write", cache.device, cache._ptr, block_table.data_ptr(), B,
+          block_table.shape[1], k.data_ptr(), *ks, v.data_ptr(), *vs, T, _ptr(start), _ptr(lens))
+    return cache
+
+
+def cache_read(cache: KVCache, block_table: torch.Tensor, lens, tokens: int, start=None,
+               out_dtype=torch.bfloat16, k=None, v=None):
+    """Rows of the cache decoded: (k, v), [batch, tokens, heads, head_dim] bf16
+    or float32; row t < lens[b] (lens None: every row) is position start[b] + t,
+    the others are zeros."""
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [batch, pages of a sequence]")
+    shape = (block_table.shape[0], int(tokens), cache.heads, cache.head_dim)
+    _cache_index(cache, block_table, shape[0], ((start, "start"), (lens, "lens")))
+    if k is None:
+        k = torch.empty(shape, dtype=out_dtype, device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=out_dtype, device=cache.device)
+    ks = _head_rows(k, out_dtype, "k", cache.device)
+    vs = _head_rows(v, out_dtype, "v", cache.device)
+    if tuple(k.shape) != shape or tuple(v.shape) != shape:
+        raise ValueError("k and v must be [batch, tokens, heads, head_dim]")
+    _disjoint_rows(k, "k")
+    _disjoint_rows(v, "v")
+    _call("kq_cache_read", cache.device, cache._ptr, block_table.data_ptr(), shape[0],
+          block_table.shape[1], shape[1], _ptr(start), _ptr(lens), k.data_ptr(), *ks, v.data_ptr(),
+          *vs, KQ_OUT_F32 if out_dtype == torch.float32 else KQ_OUT_BF16)
+    return k, v
+
+
+def attention_workspace_bytes(batch: int, M: int, heads: int, kv_heads: int, head_dim: int,
+                              max_len: int) -> int:
+    """Device workspace bytes attention_mxfp4 needs (0: none, or sizes it does
+    not take)."""
+    return int(lib().kq_attention_workspace_bytes(batch, M, heads, kv_heads, head_dim, max_len))
+
+
+def attention_mxfp4(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, lens: torch.Tensor,
+                    causal: bool = False, scale=None, max_len=None, out=None, lse=None,
+                    workspace=None):
+    """Attention of bf16 queries [batch, M, heads, head_dim] over the first
+    lens[b] positions of each sequence of the cache (causal: the queries are the
+    last M of them); heads / cache.heads query heads read one K/V head.  scale
+    defaults to head_dim^-0.5, max_len (a bound on lens) to what the block table
+    holds.  lse: an optional float32 [batch, heads, M] output.  A row that sees
+    no position gives 0, and -inf in lse.  Returns bf16 like q."""
+    qs = _head_rows(q, torch.bfloat16, "q", cache.device)
+    B, M, H, D = q.shape
+    if D != cache.head_dim or H == 0 or H % cache.heads != 0:
+        raise ValueError("q must have the cache's head_dim and a multiple of its heads")
+    if lens is None:
+        raise ValueError("lens must be int32 [batch]")
+    _cache_index(cache, block_table, B, ((lens, "lens"),))
+    room = block_table.shape[1] * cache.page_size
+    max_len = room if max_len is None else int(max_len)
+    if max_len < 1 or max_len > room:
+        raise ValueError("max_len must be from 1 to what the block table holds")
+    if out is None:
+        out = torch.empty((B, M, H, D), dtype=torch.bfloat16, device=q.device)
+    os_ = _head_rows(out, torch.bfloat16, "out", cache.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    _disjoint_rows(out, "out")
+    if lse is not None:
+        _dev_tensor(lse, torch.float32, "lse")
+        if tuple(lse.shape) != (B, H, M) or lse.device != cache.device:
+            raise ValueError("lse must be float32 [batch, heads, M] on the cache's device")
+    if B == 0 or M == 0:
+        return out
+    need = attention_workspace_bytes(B, M, H, cache.heads, D, max_len)
+    if workspace is None:
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    else:
+        _dev_tensor(workspace, torch.uint8, "workspace")
+        if workspace.device != cache.device:
+            raise ValueError("workspace must be on the cache's device")
+    _call("kq_attention_mxfp4", cache.device, q.data_ptr(), *qs, B, M, H, cache._ptr,
+          block_table.data_ptr(), block_table.shape[1], lens.data_ptr(), max_len,
+          float(D ** -0.5 if scale is None else scale), int(bool(causal)), out.data_ptr(), *os_,
+          _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel())
     return out
 
 

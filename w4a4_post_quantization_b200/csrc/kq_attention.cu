@@ -1,0 +1,642 @@
+// Attention of bf16 queries over the MXFP4 K/V cache:
+//
+//   S = scale q K^T over the positions p < len[b] (causal: and
+//       p <= len[b] - M + m for query m of M),   O = softmax(S) V.
+//
+// The positions are walked once with the running maximum and sum of the
+// softmax, all of them float32; a row that sees no position has O = 0 and a
+// log-sum-exp of -inf.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "kq_cache.cuh"
+#include "kq_internal.h"
+
+namespace kq {
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnArgs {
+  CacheView view;
+  const uint8_t *kc, *ks, *vc, *vs;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;                      // [batch][heads][M], or null
+  const int32_t* lens;
+  int64_t qb, qm, qh, ob, om, oh;  // strides in elements
+  int32_t M, D, max_len;
+  int32_t rows;                    // query rows of one K/V head: group * M
+  int32_t causal;
+  FastDiv group;                   // query heads per K/V head
+  float scale_log2;                // scale * log2(e)
+  int32_t chunk, n_chunks;         // positions per CTA, CTAs along the positions
+  float* part_o;                   // [batch][K/V head][chunk][row][Dp]
+  float2* part_ml;                 // (maximum, sum) of the same
+  int* err;
+};
+
+// Row r of a K/V head is query m = r / group of head group * hk + r % group.
+__device__ __forceinline__ int seq_len(const AttnArgs& a, int64_t b) {
+  return max(0, min(a.lens[b], a.max_len));
+}
+// Positions row r sees: [0, row_limit).
+__device__ __forceinline__ int row_limit(const AttnArgs& a, int len, int r) {
+  if (r >= a.rows) return 0;
+  return a.causal ? max(0, len - a.M + static_cast<int>(a.group.div(r)) + 1) : len;
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Four pairs of codes out of a word: pair i is nibble i of the low half and
+// nibble i of the high half, as bf16 bits.  A code's sign goes to bit 15 and
+// its exponent and mantissa (two bits and one) to bits 8..6, the low end of
+// bf16's fields, where they mean the code's value times 2^-126: the exponent
+// 0 of E2M1 is bf16's own subnormal.  mx_pair puts the factor right together
+// with the block's scale.
+__device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&p)[4]) {
+  p[0] = ((w << 6) & 0x01C001C0u) | ((w << 12) & 0x80008000u);
+  p[1] = ((w << 2) & 0x01C001C0u) | ((w << 8) & 0x80008000u);
+  p[2] = ((w >> 2) & 0x01C001C0u) | ((w << 4) & 0x80008000u);
+  p[3] = ((w >> 6) & 0x01C001C0u) | (w & 0x80008000u);
+}
+
+// bf16 bits of 2^(s - 63) for scale byte s <= 190: a raw code times it is the
+// value times 2^-62, exactly (2^-126 of the raw bits, 2^(s - 127) of the
+// scale).  The 2^62 keeps the multiplier in bf16's range for every scale byte
+// up to 190 (values below 2^66).  It is undone in the scores' scale, and in the
+// softmax weights, which are held as 2^62 exp2(.): their products with V then
+// have V's own range, so small weights are not lost to underflow.
+__device__ __forceinline__ uint32_t mx_mul(uint32_t s) { return (s + 64) << 7; }
+constexpr int kShift = 62;
+constexpr float kUnscale = 4611686018427387904.0f;      // 2^kShift
+
+// ---------------------------------------------------------------------------
+// Few query rows: one warp walks 32 positions at a time with mma.sync, its
+// operands decoded in registers.  The rows fill (part of) the MMA's 16, so the
+// cost is the cache's bytes and their decoding, whatever the group.
+//
+// Lane (g, c) = (lane / 4, lane mod 4).  The products contract over the head's
+// channels (S) and the positions (O) in any order, as long as both operands
+// use the same one, so each lane takes what is contiguous for it:
+//   K  lane c's quarter of the row of position n = g, one 4-byte word being the
+//      channels of two MMA k-steps,
+//   V  for positions c, c + 4, c + 8, c + 12 of 16, the g-th eighth of the row.
+// No shuffle and no transpose lies between the cache's bytes and the MMA.
+constexpr int kWarps = 4;
+constexpr int kTile = 32;                     // positions a warp holds at a time
+constexpr int kStages = 4;
+
+template <int kW>                             // 32-channel blocks of a row
+struct SplitGeom {
+  static constexpr int kDp = 32 * kW;
+  static constexpr int kCodes = kTile * kDp / 2;
+  static constexpr int kScales = kTile * kW;
+  static constexpr int kStage = 2 * kCodes + 2 * kScales;
+  static constexpr int kRing = kWarps * kStages * kStage;
+};
+template <int kW, int kMT>
+constexpr int split_smem() {
+  const int merge = kWarps * 16 * kMT * (32 * kW + 2) * 4;
+  return merge > SplitGeom<kW>::kRing ? merge : SplitGeom<kW>::kRing;
+}
+
+template <int kW, int kMT>
+__global__ void __launch_bounds__(32 * kWarps) attn_split_kernel(const AttnArgs a) {
+  using G = SplitGeom<kW>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int chunk = blockIdx.x % a.n_chunks, r0 = blockIdx.x / a.n_chunks * (16 * kMT);
+  const int hk = blockIdx.y;
+  const int64_t b = blockIdx.z;
+  pdl_wait_then_trigger();
+
+  const int len = seq_len(a, b);
+  const int first_limit = row_limit(a, len, r0);                       // the fewest a row sees
+  const int last_limit = row_limit(a, len, min(r0 + 16 * kMT, a.rows) - 1);
+  const int begin = chunk * a.chunk;
+  const int end = min(begin + a.chunk, last_limit);
+  int limit[kMT][2];
+#pragma unroll
+  for (int t = 0; t < kMT; ++t) {
+    limit[t][0] = row_limit(a, len, r0 + 16 * t + g);
+    limit[t][1] = row_limit(a, len, r0 + 16 * t + g + 8);
+  }
+
+  // Queries as A fragments, in the channel order of the K words.
+  uint32_t q[kMT][2 * kW][4];
+#pragma unroll
+  for (int t = 0; t < kMT; ++t)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = r0 + 16 * t + g + 8 * hf;
+      const int m = a.group.div(r), h = hk * a.group.d + r - m * a.group.d;
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        const int d0 = (c * kW + j) * 8;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < a.rows && d0 < a.D)
+          x = __ldg(reinterpret_cast<const uint4*>(a.q + b * a.qb + m * a.qm + h * a.qh + d0));
+        q[t][2 * j][hf] = __byte_perm(x.x, x.z, 0x5410);
+        q[t][2 * j][2 + hf] = __byte_perm(x.x, x.z, 0x7632);
+        q[t][2 * j + 1][hf] = __byte_perm(x.y, x.w, 0x5410);
+        q[t][2 * j + 1][2 + hf] = __byte_perm(x.y, x.w, 0x7632);
+      }
+    }
+
+  float o[kMT][4 * kW][4], mx[kMT][2], l[kMT][2];
+#pragma unroll
+  for (int t = 0; t < kMT; ++t) {
+#pragma unroll
+    for (int n = 0; n < 4 * kW; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[t][n][k] = 0.0f;
+    mx[t][0] = mx[t][1] = -INFINITY;
+    l[t][0] = l[t][1] = 0.0f;
+  }
+
+  // This warp's tiles: positions begin + 32 (warp + 4 i).
+  const int n_tiles = end > begin + kTile * warp
+                          ? (end - begin - kTile * warp + kTile * kWarps - 1) / (kTile * kWarps) : 0;
+  uint8_t* ring = smem + warp * (kStages * G::kStage);
+  auto tile_pos = [&](int i) { return begin + kTile * (warp + kWarps * i); };
+  // Pages of 16 tiles at a time, lane 2 i + half holding half `half` of tile
+  // i: the table is read once, ahead of the loads that need it.  -1: nothing
+  // to load there.
+  int page = -1;
+  auto load_pages = [&](int i) {
+    const int pos = tile_pos(i + (lane >> 1)) + 16 * (lane & 1);
+    page = -1;
+    if (i + (lane >> 1) < n_tiles && pos < end) {
+      const int at = pos >> a.view.page_shift;
+      if (at < a.view.table_pages) page = __ldg(a.view.table + b * a.view.table_pages + at);
+      if (page < 0 || page >= a.view.pages) {
+        page = -1;
+        atomicOr(a.err, kErrCacheIndex);
+      }
+    }
+  };
+  uint32_t absent = 0;                        // bit 2 (i mod 4) + half: that half has no page
+  auto load_tile = [&](int i) {
+    if (i < n_tiles) {
+      if ((i & 15) == 0) load_pages(i);
+      uint8_t* st = ring + (i % kStages) * G::kStage;
+      const int pos = tile_pos(i);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int p = __shfl_sync(0xFFFFFFFFu, page, 2 * (i & 15) + half);
+        const uint32_t bit = 1u << (2 * (i % kStages) + half);
+        absent = p < 0 ? absent | bit : absent & ~bit;
+        if (p >= 0) {
+          const int64_t row = ((static_cast<int64_t>(p) * a.view.heads + hk) << a.view.page_shift) +
+                              ((pos + 16 * half) & ((1 << a.view.page_shift) - 1));
+          const uint8_t* kc = a.kc + row * (G::kDp / 2);
+          const uint8_t* vc = a.vc + row * (G::kDp / 2);
+          uint8_t* dk = st + half * (G::kCodes / 2);
+#pragma unroll
+          for (int j = 0; j < (G::kCodes / 2 + 511) / 512; ++j) {
+            const int off = 16 * lane + 512 * j;
+            if (off < G::kCodes / 2) {
+              cp_async16(dk + off, kc + off);
+              cp_async16(dk + G::kCodes + off, vc + off);
+            }
+          }
+          if (lane < 2 * kW) {
+            const bool v = lane >= kW;
+            const int off = 16 * (v ? lane - kW : lane);
+            cp_async16(st + 2 * G::kCodes + v * G::kScales + half * (G::kScales / 2) + off,
+                       (v ? a.vs : a.ks) + row * kW + off);
+          }
+        }
+      }
+    }
+    cp_async_commit();
+  };
+
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load_tile(i);
+
+  for (int i = 0; i < n_tiles; ++i) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();
+    const uint32_t gone = (absent >> (2 * (i % kStages))) & 3u;
+    load_tile(i + kStages - 1);               // into the stage read in the last step
+    const uint8_t* st = ring + (i % kStages) * G::kStage;
+    const uint8_t* ksc = st + 2 * G::kCodes;
+    const uint8_t* vsc = ksc + G::kScales;
+    const int pos = tile_pos(i);
+
+    // S of 32 positions.
+    float s[kMT][4][4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+#pragma unroll
+      for (int t = 0; t < kMT; ++t)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[t][n][k] = 0.0f;
+      const int tok = 8 * n + (g >> 1) + 4 * (g & 1);
+      uint32_t w[kW];
+      const uint32_t* kw = reinterpret_cast<const uint32_t*>(st + tok * (G::kDp / 2)) + c * kW;
+      if constexpr (kW == 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(kw);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+      } else if constexpr (kW == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(kw);
+        w[0] = x.x, w[1] = x.y;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kW; ++j) w[j] = kw[j];
+      }
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        const uint32_t m2 = mx_mul(ksc[tok * kW + ((c * kW + j) >> 2)]) * 0x10001u;
+        uint32_t p[4];
+        e2m1_pairs(w[j], p);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = mul_bf16x2(p[k], m2);
+#pragma unroll
+        for (int t = 0; t < kMT; ++t) {
+          mma_bf16(s[t][n], q[t][2 * j], p[0], p[1]);
+          mma_bf16(s[t][n], q[t][2 * j + 1], p[2], p[3]);
+        }
+      }
+    }
+
+    // Running maximum and sum.  Column 2 c of tile n is position 8 n + c,
+    // column 2 c + 1 position 8 n + c + 4 (16 positions: 8 n -> 16 half + 8).
+    const bool ragged = pos + kTile > first_limit || gone;
+    uint32_t pa[kMT][2][4];
+#pragma unroll
+    for (int t = 0; t < kMT; ++t) {
+      const float sc = a.scale_log2 * kUnscale;
+      float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float v = s[t][n][k] * sc;
+          if (ragged) {
+            const int p = pos + 8 * n + c + 4 * (k & 1);
+            if (p >= limit[t][k >> 1] || (gone >> (n >> 1) & 1)) v = -INFINITY;
+          }
+          s[t][n][k] = v;
+          top[k >> 1] = fmaxf(top[k >> 1], v);
+        }
+      bool grew = false;
+      float base[2], alpha[2];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xFFFFFFFFu, top[hf], 1));
+        top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xFFFFFFFFu, top[hf], 2));
+        const float m_new = fmaxf(mx[t][hf], top[hf]);
+        // A row that has seen nothing yet: exp2(-inf - 0) = 0.
+        base[hf] = m_new == -INFINITY ? 0.0f : m_new;
+        alpha[hf] = ex2(mx[t][hf] - base[hf]);
+        base[hf] -= kShift;
+        grew |= m_new > mx[t][hf];
+        mx[t][hf] = m_new;
+      }
+      if (__any_sync(0xFFFFFFFFu, grew)) {
+#pragma unroll
+        for (int n = 0; n < 4 * kW; ++n)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[t][n][k] *= alpha[k >> 1];
+        l[t][0] *= alpha[0];
+        l[t][1] *= alpha[1];
+      }
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[t][n][k] = ex2(s[t][n][k] - base[k >> 1]);
+          l[t][k >> 1] += s[t][n][k];
+        }
+        // The weights are rounded to bf16, the type of the product (each by at
+        // most 2^-8 of itself); their sum is taken before.
+        pa[t][n >> 1][2 * (n & 1)] = bf16x2(s[t][n][0], s[t][n][1]);
+        pa[t][n >> 1][2 * (n & 1) + 1] = bf16x2(s[t][n][2], s[t][n][3]);
+      }
+    }
+
+    // O += P V.
+    const bool tail = pos + kTile > len || gone;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t hw[4][(kW + 1) / 2];           // two 4-channel units a word
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint8_t* vp = st + G::kCodes + (16 * half + c + 4 * k) * (G::kDp / 2) + g * 2 * kW;
+        if constexpr (kW == 4) {
+          const uint2 x = *reinterpret_cast<const uint2*>(vp);
+          hw[k][0] = x.x, hw[k][1] = x.y;
+        } else if constexpr (kW == 2) {
+          hw[k][0] = *reinterpret_cast<const uint32_t*>(vp);
+        } else {
+          const uint16_t* vh = reinterpret_cast<const uint16_t*>(vp);
+          hw[k][0] = vh[0];
+          if constexpr (kW == 3) {
+            hw[k][0] |= static_cast<uint32_t>(vh[1]) << 16;
+            hw[k][1] = vh[2];
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kW; ++u) {
+        uint32_t m[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tok = 16 * half + c + 4 * k;
+          m[k] = mx_mul(vsc[tok * kW + ((g * kW + u) >> 3)]);
+          // What lies behind the sequence is unknown: its codes times zero.
+          if (tail && (pos + tok >= len || (gone >> half & 1))) m[k] = 0;
+        }
+        const uint32_t m01 = m[0] | m[1] << 16, m23 = m[2] | m[3] << 16;
+        const uint32_t sel = u & 1 ? 0x7632 : 0x5410;
+        uint32_t x[4], y[4];
+        e2m1_pairs(__byte_perm(hw[0][u >> 1], hw[1][u >> 1], sel), x);
+        e2m1_pairs(__byte_perm(hw[2][u >> 1], hw[3][u >> 1], sel), y);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t b0 = mul_bf16x2(x[k], m01), b1 = mul_bf16x2(y[k], m23);
+#pragma unroll
+          for (int t = 0; t < kMT; ++t) mma_bf16(o[t][4 * u + k], pa[t][half], b0, b1);
+        }
+      }
+    }
+    __syncwarp();
+  }
+  cp_async_wait<0>();
+
+  // The four warps' parts, joined in a fixed order.
+#pragma unroll
+  for (int t = 0; t < kMT; ++t)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      l[t][hf] += __shfl_xor_sync(0xFFFFFFFFu, l[t][hf], 1);
+      l[t][hf] += __shfl_xor_sync(0xFFFFFFFFu, l[t][hf], 2);
+    }
+  __syncthreads();
+  constexpr int kRows = 16 * kMT;
+  float* so = reinterpret_cast<float*>(smem);                    // [warp][row][Dp]
+  float2* sml = reinterpret_cast<float2*>(so + kWarps * kRows * G::kDp);
+#pragma unroll
+  for (int t = 0; t < kMT; ++t)
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int r = 16 * t + g + 8 * hf;
+      float* dst = so + (warp * kRows + r) * G::kDp;
+      // Column n of MMA tile j is channel n (Dp / 8) + j.
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int u = 0; u < kW; ++u)
+          *reinterpret_cast<float4*>(dst + (2 * c + e) * 4 * kW + 4 * u) =
+              make_float4(o[t][4 * u][2 * hf + e], o[t][4 * u + 1][2 * hf + e],
+                          o[t][4 * u + 2][2 * hf + e], o[t][4 * u + 3][2 * hf + e]);
+      if (c == 0) sml[warp * kRows + r] = make_float2(mx[t][hf], l[t][hf]);
+    }
+  __syncthreads();
+  for (int i = tid; i < kRows * (G::kDp / 4); i += 32 * kWarps) {
+    const int r = i / (G::kDp / 4), d = 4 * (i - r * (G::kDp / 4));
+    if (r0 + r >= a.rows) break;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sml[w * kRows + r].x);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 ml = sml[w * kRows + r];
+      const float k = ex2(ml.x - base);
+      const float4 x = *reinterpret_cast<const float4*>(so + (w * kRows + r) * G::kDp + d);
+      sum += k * ml.y;
+      acc.x += k * x.x, acc.y += k * x.y, acc.z += k * x.z, acc.w += k * x.w;
+    }
+    if (a.n_chunks > 1) {
+      const int64_t at = ((b * a.view.heads + hk) * a.n_chunks + chunk) * a.rows + r0 + r;
+      if (top != -INFINITY) *reinterpret_cast<float4*>(a.part_o + at * G::kDp + d) = acc;
+      if (d == 0) a.part_ml[at] = make_float2(top, sum);
+      continue;
+    }
+    const int m = a.group.div(r0 + r), h = hk * a.group.d + r0 + r - m * a.group.d;
+    const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+    if (d < a.D)
+      *reinterpret_cast<uint2*>(a.out + b * a.ob + m * a.om + h * a.oh + d) =
+          make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
+    if (a.lse && d == 0)
+      a.lse[(b * a.view.heads * a.group.d + h) * a.M + m] =
+          top == -INFINITY ? -INFINITY : (top + (log2f(sum) - kShift)) * kLn2;
+  }
+}
+
+// Joins the chunks of each row: a warp per row.
+template <int kW>
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int64_t n_rows) {
+  pdl_wait_then_trigger();
+  const int lane = threadIdx.x & 31;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (at >= n_rows) return;
+  const int64_t bh = at / a.rows;
+  const int r = static_cast<int>(at - bh * a.rows);
+  const int64_t b = bh / a.view.heads;
+  const int hk = static_cast<int>(bh - b * a.view.heads);
+  const int n = (row_limit(a, seq_len(a, b), r) + a.chunk - 1) / a.chunk;
+  const float2* ml = a.part_ml + bh * a.n_chunks * a.rows + r;
+  const float* po = a.part_o + (bh * a.n_chunks * a.rows + r) * (32 * kW);
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[static_cast<int64_t>(i) * a.rows].x);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+  const float base = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f, acc[kW];
+#pragma unroll
+  for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float2 x = ml[static_cast<int64_t>(i) * a.rows];
+    const float k = ex2(x.x - base);
+    sum += k * x.y;
+    // A chunk in which the row sees nothing has written no O.
+    if (x.x != -INFINITY)
+#pragma unroll
+      for (int j = 0; j < kW; ++j)
+        acc[j] += k * po[static_cast<int64_t>(i) * a.rows * (32 * kW) + 32 * j + lane];
+  }
+  const int m = a.group.div(r), h = hk * a.group.d + r - m * a.group.d;
+  const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+  uint16_t* dst = a.out + b * a.ob + m * a.om + h * a.oh;
+#pragma unroll
+  for (int j = 0; j < kW; ++j)
+    if (32 * j + lane < a.D)
+      dst[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[j] * inv));
+  if (a.lse && lane == 0)
+    a.lse[(b * a.view.heads * a.group.d + h) * a.M + m] =
+        top == -INFINITY ? -INFINITY : (top + (log2f(sum) - kShift)) * kLn2;
+}
+
+// How a call is cut: from its sizes alone, so that the workspace query and the
+// call agree.
+struct Plan {
+  int row_groups, mt;
+  int64_t chunk, n_chunks;
+  size_t ml_bytes, bytes;
+};
+
+Plan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int nb) {
+  Plan p{};
+  p.mt = rows > 16 ? 2 : 1;
+  p.row_groups = static_cast<int>((rows + 16 * p.mt - 1) / (16 * p.mt));
+  constexpr int64_t kStep = kTile * kWarps;
+  // About eight CTAs for each of the 148 SMs, of at least 512 positions.
+  const int64_t units = batch * kv_heads * p.row_groups;
+  const int64_t want = std::max<int64_t>(1, 8 * 148 / units);
+  int64_t chunk = std::max<int64_t>(512, (max_len + want - 1) / want);
+  chunk = (chunk + kStep - 1) / kStep * kStep;
+  p.chunk = chunk;
+  p.n_chunks = std::max<int64_t>(1, (max_len + chunk - 1) / chunk);
+  if (p.n_chunks > 1) {
+    const int64_t parts = batch * kv_heads * p.n_chunks * rows;
+    p.ml_bytes = static_cast<size_t>((parts * 8 + 255) / 256 * 256);
+    p.bytes = p.ml_bytes + static_cast<size_t>(parts) * nb * 32 * 4;
+  }
+  return p;
+}
+
+template <int kW, int kMT>
+int launch_split(const AttnArgs& a, const Plan& p, int64_t batch, int dev, cudaStream_t st) {
+  constexpr int smem = split_smem<kW, kMT>();
+  const int rc = allow_smem<attn_split_kernel<kW, kMT>>(smem, dev);
+  if (rc != KQ_OK) return rc;
+  const dim3 grid(static_cast<unsigned>(p.n_chunks * p.row_groups),
+                  static_cast<unsigned>(a.view.heads), static_cast<unsigned>(batch));
+  cudaError_t e = launch_pdl(attn_split_kernel<kW, kMT>, grid, dim3(32 * kWarps), smem, st, a);
+  if (e != cudaSuccess) return record_cuda_error(e);
+  if (a.n_chunks > 1) {
+    const int64_t n_rows = batch * a.view.heads * a.rows;
+    e = launch_pdl(attn_join_kernel<kW>, dim3(static_cast<unsigned>((n_rows + 3) / 4)), dim3(128), 0,
+                   st, a, n_rows);
+    if (e != cudaSuccess) return record_cuda_error(e);
+  }
+  return KQ_OK;
+}
+
+template <int kW>
+int launch_split_mt(const AttnArgs& a, const Plan& p, int64_t batch, int dev, cudaStream_t st) {
+  return p.mt == 1 ? launch_split<kW, 1>(a, p, batch, dev, st) : launch_split<kW, 2>(a, p, batch, dev, st);
+}
+
+// Sizes a call can have: 0 where they are not valid, else the rows of a K/V
+// head.
+int64_t attention_rows(int64_t batch, int64_t M, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                       int64_t max_len) {
+  if (batch < 1 || batch > 65535 || M < 1 || heads < 1 || kv_heads < 1 || kv_heads > 65535 ||
+      heads % kv_heads != 0 || head_dim < 8 || head_dim > 128 || head_dim % 8 != 0 || max_len < 1 ||
+      max_len >= (int64_t(1) << 31) - 65536)
+    return 0;
+  if (M > (int64_t(1) << 30) || heads > (int64_t(1) << 30)) return 0;
+  const int64_t rows = M * (heads / kv_heads);
+  return rows <= (int64_t(1) << 30) && batch * kv_heads <= (int64_t(1) << 31) / rows ? rows : 0;
+}
+
+}  // namespace
+}  // namespace kq
+
+using namespace kq;
+
+extern "C" size_t kq_attention_workspace_bytes(int64_t batch, int64_t M, int64_t heads,
+                                               int64_t kv_heads, int64_t head_dim, int64_t max_len) {
+  const int64_t rows = attention_rows(batch, M, heads, kv_heads, head_dim, max_len);
+  if (rows == 0) return 0;
+  return make_plan(batch, kv_heads, rows, max_len, static_cast<int>((head_dim + 31) / 32)).bytes;
+}
+
+extern "C" int kq_attention_mxfp4(const uint16_t* q, int64_t q_sb, int64_t q_sm, int64_t q_sh,
+                                  int64_t batch, int64_t M, int64_t heads, const kq_cache* cache,
+                                  const int32_t* block_table, int64_t table_pages,
+                                  const int32_t* lens, int64_t max_len, float scale, int causal,
+                                  uint16_t* out, int64_t o_sb, int64_t o_sm, int64_t o_sh,
+                                  float* lse, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  if (batch < 0 || M < 0) return KQ_ERR_INVALID;
+  if (batch == 0 || M == 0) return KQ_OK;
+  AttnArgs a{};
+  if (!cache_view(cache, block_table, batch, table_pages, &a.view)) return KQ_ERR_INVALID;
+  const int64_t rows = attention_rows(batch, M, heads, cache->heads, cache->head_dim, max_len);
+  if (rows == 0 || max_len > table_pages * cache->page_size) return KQ_ERR_INVALID;
+  auto al = [](const void* p, uintptr_t n) { return p && reinterpret_cast<uintptr_t>(p) % n == 0; };
+  auto strides = [](int64_t x, int64_t y, int64_t z) {
+    return x >= 0 && y >= 0 && z >= 0 && x % 8 == 0 && y % 8 == 0 && z % 8 == 0;
+  };
+  if (!al(q, 16) || !al(out, 16) || !al(lens, 4) || !strides(q_sb, q_sm, q_sh) ||
+      !strides(o_sb, o_sm, o_sh) || (lse && !al(lse, 4)) || !std::isfinite(scale))
+    return KQ_ERR_INVALID;
+  const Plan p = make_plan(batch, cache->heads, rows, max_len, a.view.nb);
+  if (p.bytes > 0 && (!al(workspace, 256) || workspace_bytes < p.bytes)) return KQ_ERR_INVALID;
+  if (p.n_chunks * p.row_groups >= (int64_t(1) << 31)) return KQ_ERR_INVALID;
+  const DeviceInfo* di = nullptr;
+  int dev = 0;
+  int rc = device_info(&di, &dev);
+  if (rc != KQ_OK) return rc;
+  rc = device_error_word(dev, &a.err);
+  if (rc != KQ_OK) return rc;
+  a.kc = cache->k_codes, a.ks = cache->k_scales, a.vc = cache->v_codes, a.vs = cache->v_scales;
+  a.q = q, a.qb = q_sb, a.qm = q_sm, a.qh = q_sh;
+  a.out = out, a.ob = o_sb, a.om = o_sm, a.oh = o_sh;
+  a.lse = lse;
+  a.lens = lens;
+  a.M = static_cast<int32_t>(M);
+  a.D = static_cast<int32_t>(cache->head_dim);
+  a.max_len = static_cast<int32_t>(max_len);
+  a.rows = static_cast<int32_t>(rows);
+  a.causal = causal != 0;
+  a.group = FastDiv(static_cast<uint32_t>(heads / cache->heads));
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.chunk = static_cast<int32_t>(p.chunk);
+  a.n_chunks = static_cast<int32_t>(p.n_chunks);
+  a.part_ml = static_cast<float2*>(workspace);
+  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.ml_bytes);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  switch (a.view.nb) {
+    case 1: return launch_split_mt<1>(a, p, batch, dev, st);
+    case 2: return launch_split_mt<2>(a, p, batch, dev, st);
+    case 3: return launch_split_mt<3>(a, p, batch, dev, st);
+    default: return launch_split_mt<4>(a, p, batch, dev, st);
+  }
+}

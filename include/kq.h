@@ -262,6 +262,32 @@ int kq_gemm_mxfp4_tiled(const uint8_t* qa, const uint8_t* sa_tiled, const uint8_
                         const uint8_t* sb_tiled, int64_t M, int64_t N, int64_t K, void* c,
                         int c_dtype, void* stream);
 
+/* Activations of kq_gemm_mxfp4_epilogue. */
+enum {
+    KQ_ACT_NONE = 0,
+    KQ_ACT_GELU_TANH = 1,   /* 0.5 y (1 + tanh(sqrt(2/pi) (y + 0.044715 y^3))) */
+    KQ_ACT_GELU = 2,        /* y Phi(y) */
+    KQ_ACT_SILU = 3         /* y / (1 + exp(-y)) */
+};
+
+/* kq_gemm_mxfp4_tiled with what follows a transformer layer's product applied
+ * to the float32 accumulator, rounded once at the end:
+ *   c[m][n] = residual[m][n] + gate[m / tokens_per_sample][n]
+ *                              * act((A B^T)[m][n] + bias[n])
+ * bias, gate and residual may each be NULL (0, 1, 0).
+ *   bias: bf16 [N]; gate: bf16 [ceil(M / tokens_per_sample)][N], the AdaLN gate
+ *   of each sample (tokens_per_sample >= 1 where there is a gate); residual:
+ *   [M][N] of c's type, which may be c itself (c += ...) and must not overlap it
+ *   otherwise.  All 16-byte aligned; operands, c and c_dtype as for
+ *   kq_gemm_mxfp4_tiled, M, N and K below 2^31 - 512.  Rows whose N is a
+ *   multiple of 8 take the fast path out.  An activation is within 2e-6 times
+ *   the larger of |y| and 1 of its value at the float32 y. */
+int kq_gemm_mxfp4_epilogue(const uint8_t* qa, const uint8_t* sa_tiled, const uint8_t* qb,
+                           const uint8_t* sb_tiled, int64_t M, int64_t N, int64_t K,
+                           const uint16_t* bias, int activation, const uint16_t* gate,
+                           int64_t tokens_per_sample, const void* residual, void* c, int c_dtype,
+                           void* stream);
+
 /* Bytes of the tiled scale layout for `rows` rows of K/32 scales (0 for an
  * invalid K or rows < 1). */
 size_t kq_scales_tiled_bytes(int64_t rows, int64_t K);

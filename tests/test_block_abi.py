@@ -123,3 +123,23 @@ def test_overlapping_output_rows_are_refused(L):
         else:
             with pytest.raises(ValueError):
                 L._disjoint_rows(t, "out")
+
+
+def epilogue(L, qa=FAKE, sa=FAKE, qb=FAKE, sb=FAKE, M=4, N=8, K=64, bias=None, act=0, gate=None, tokens=0,
+             residual=None, c=FAKE, dtype=1):
+    return L.lib().kq_gemm_mxfp4_epilogue(qa, sa, qb, sb, M, N, K, bias, act, gate, tokens, residual, c,
+                                          dtype, None)
+
+
+@pytest.mark.parametrize("bad", [dict(qa=None), dict(qa=FAKE + 8), dict(sa=FAKE + 4), dict(qb=FAKE + 1),
+                                 dict(sb=None), dict(M=-1), dict(N=-1), dict(K=0), dict(K=48),
+                                 dict(M=(1 << 31) - 1), dict(M=1 << 30, N=1 << 30), dict(bias=FAKE + 2),
+                                 dict(act=-1), dict(act=4), dict(gate=FAKE, tokens=0),
+                                 dict(gate=FAKE + 2, tokens=4), dict(residual=FAKE + 4), dict(c=None),
+                                 dict(c=FAKE + 8), dict(dtype=2)], ids=str)
+def test_bad_epilogue(L, bad):
+    assert epilogue(L, **bad) == 1
+
+
+def test_empty_epilogue_needs_no_device(L):
+    assert epilogue(L, M=0, qa=None, c=None) == 0 and epilogue(L, N=0, qb=None, c=None) == 0

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libkq.so")
 KQ_OK, KQ_ERR_INVALID, KQ_ERR_CUDA, KQ_ERR_DEVICE, KQ_ERR_TIMEOUT = 0, 1, 2, 3, 4
 KQ_IMPL_AUTO, KQ_IMPL_TMA, KQ_IMPL_DIRECT, KQ_IMPL_WARP, KQ_IMPL_PANEL, KQ_IMPL_MMA = 0, 1, 2, 3, 4, 5
 KQ_OUT_F32, KQ_OUT_BF16 = 0, 1
+ACTIVATIONS = {"none": 0, "gelu_tanh": 1, "gelu": 2, "silu": 3}
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -43,6 +44,8 @@ SIGNATURES = {
     "kq_fold_weight": [_p, _i64, _i64, _p, _p, _p],
     "kq_gemm_mxfp4": [_p, _p, _p, _p, _i64, _i64, _i64, _p, _int, _p],
     "kq_gemm_mxfp4_tiled": [_p, _p, _p, _p, _i64, _i64, _i64, _p, _int, _p],
+    "kq_gemm_mxfp4_epilogue": [_p, _p, _p, _p, _i64, _i64, _i64, _p, _int, _p, _i64, _p, _p, _int,
+                               _p],
     "kq_scales_tiled_bytes": [_i64, _i64],
     "kq_quantize_tiled": [_p, _i64, _i64, _p, _p, _p, _p],
     "kq_quantize_weight_tiled": [_p, _i64, _i64, _p, _p, _p, _p],
@@ -587,6 +590,60 @@ def gemm_mxfp4_tiled(qa: torch.Tensor, sa_tiled: torch.Tensor, qb: torch.Tensor,
                                    sb_tiled.data_ptr(), M, N, K, out.data_ptr(), code,
                                    _stream(qa.device))
     _check("kq_gemm_mxfp4_tiled", st)
+    return out
+
+
+def gemm_mxfp4_epilogue(qa: torch.Tensor, sa_tiled: torch.Tensor, qb: torch.Tensor,
+                        sb_tiled: torch.Tensor, bias=None, activation: str = "none", gate=None,
+                        tokens_per_sample=None, residual=None, out=None,
+                        out_dtype=torch.bfloat16):
+    """residual + gate[m // tokens_per_sample] * act(A B^T + bias), each part
+    optional, rounded once: gemm_mxfp4_tiled with the rest of a transformer
+    layer's product.  bias bf16 [N]; activation "none", "gelu_tanh", "gelu" or
+    "silu"; gate bf16 [samples, N] with samples >= ceil(M / tokens_per_sample);
+    residual [M, N] of out's type, and ``out=residual`` adds in place."""
+    for t, n in ((qa, "qa"), (sa_tiled, "sa_tiled"), (qb, "qb"), (sb_tiled, "sb_tiled")):
+        _dev_tensor(t, torch.uint8, n)
+    if qa.dim() != 2 or qb.dim() != 2 or qa.shape[1] == 0 or qa.shape[1] % 16 != 0:
+        raise ValueError("qa must be [M, K/2] and qb [N, K/2], K a multiple of 32")
+    M, K = qa.shape[0], 2 * qa.shape[1]
+    N = qb.shape[0]
+    if qb.shape[1] != K // 2:
+        raise ValueError("qb must be [N, K/2]")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    size = lib().kq_scales_tiled_bytes
+    if sa_tiled.numel() < size(M, K) or sb_tiled.numel() < size(N, K):
+        raise ValueError("tiled scale arrays are too small")
+    if bias is not None:
+        _dev_tensor(bias, torch.bfloat16, "bias")
+        if tuple(bias.shape) != (N,):
+            raise ValueError("bias must be bf16 [N]")
+    if gate is not None:
+        _dev_tensor(gate, torch.bfloat16, "gate")
+        if tokens_per_sample is None or int(tokens_per_sample) < 1:
+            raise ValueError("a gate needs tokens_per_sample >= 1")
+        if gate.dim() != 2 or gate.shape[1] != N or gate.shape[0] < -(-M // int(tokens_per_sample)):
+            raise ValueError("gate must be bf16 [B, N] with B >= ceil(M / tokens_per_sample)")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=qa.device)
+    for t, n in ((out, "out"), (residual, "residual")):
+        if t is not None:
+            _dev_tensor(t, out_dtype, n)
+            if tuple(t.shape) != (M, N):
+                raise ValueError(f"{n} must be [M, N]")
+    if residual is not None and M * N and residual.data_ptr() != out.data_ptr() and \
+            abs(residual.data_ptr() - out.data_ptr()) < M * N * out.element_size():
+        raise ValueError("residual must be out itself or not overlap it")
+    for t in (sa_tiled, qb, sb_tiled, bias, gate, residual, out):
+        if t is not None and t.device != qa.device:
+            raise ValueError("the operands must be on one device")
+    _call("kq_gemm_mxfp4_epilogue", qa.device, qa.data_ptr(), sa_tiled.data_ptr(), qb.data_ptr(),
+          sb_tiled.data_ptr(), M, N, K, _ptr(bias), ACTIVATIONS[activation], _ptr(gate),
+          0 if gate is None else int(tokens_per_sample), _ptr(residual), out.data_ptr(),
+          KQ_OUT_F32 if out_dtype == torch.float32 else KQ_OUT_BF16)
     return out
 
 

@@ -34,24 +34,14 @@
 
 #include "kq.h"
 #include "kq_device.cuh"
+#include "kq_gemm.cuh"
 #include "kq_internal.h"
 #include "kq_tc.cuh"
 
 namespace kq {
 namespace {
 
-constexpr int kBM = 128;                       // UMMA M: rows of A per tile
-constexpr int kBN = 256;                       // UMMA N: rows of B per tile
-constexpr int kBK = 256;                       // K elements per stage
-constexpr int kBKBytes = kBK / 2;              // 128 bytes of codes per row
-constexpr int kMmaK = 64;                      // K elements per MMA
 constexpr int kStages = 4;
-constexpr int kATile = kBM * kBKBytes;         // 16 KiB
-constexpr int kBTile = kBN * kBKBytes;         // 32 KiB
-constexpr int kSfChunk = 512;                  // 128 rows x 4 scale bytes
-constexpr int kChunksPerStage = kBK / 128;     // 2 chunks of 4 scales per row
-constexpr int kSfaBytes = kChunksPerStage * kSfChunk;
-constexpr int kSfbBytes = kChunksPerStage * (kBN / 128) * kSfChunk;
 constexpr int kStageBytes = kATile + kBTile + kSfaBytes + kSfbBytes;
 static_assert(kStageBytes % 1024 == 0, "stages must keep the 1024-byte swizzle alignment");
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes + (2 * kStages + 2) * 8 + 16;
@@ -61,17 +51,10 @@ static_assert(kBN * 4 / 128 * kOutBoxBytes <= kStages * kStageBytes, "output til
 constexpr int kSfWarp0 = 6;                    // warps 6..9 load scales, one stage each
 constexpr int kSfWarps = kStages;
 constexpr int kGemmThreads = 32 * (kSfWarp0 + kSfWarps);
-constexpr int kBandN = 16;                     // column tiles per raster band
 // Scale words (4 bytes) per stage: 2 per row of A and of B.
 constexpr int kSfWordsPerStage = (kBM + kBN) * kChunksPerStage;
 constexpr int kSfWordsPerLane = kSfWordsPerStage / 32;
 
-// TMEM: the accumulator in columns [0, 256), then per stage 4 columns per
-// scale chunk of A and 8 per chunk of B (two 128-row groups).
-constexpr int kSfColsA = 4 * kChunksPerStage;
-constexpr int kSfColsB = 8 * kChunksPerStage;
-constexpr int kSfCol0 = kBN;
-constexpr int kTmemCols = 512;
 static_assert(kSfCol0 + kStages * (kSfColsA + kSfColsB) <= kTmemCols, "TMEM columns");
 
 // Instruction descriptor, block-scaled kinds: A and B E2M1 (format 1 of
@@ -102,20 +85,6 @@ __device__ __forceinline__ void mma_mxf4(uint32_t tmem_d, uint64_t adesc, uint64
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;"
-      "\n\t}" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(tsfa), "r"(tsfb)
-      : "memory");
-}
-
-// The same MMA over a CTA pair (M = 256): issued by the even CTA, A rows and
-// accumulator rows 0..127 in it and 128..255 in the odd one, B's N rows split
-// 128 / 128 between their shared memories, each CTA's scales in its TMEM.
-__device__ __forceinline__ void mma_mxf4_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
-                                              uint32_t idesc, uint32_t tsfa, uint32_t tsfb,
-                                              uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;"
       "\n\t}" ::"r"(tmem_d),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(tsfa), "r"(tsfb)
       : "memory");
@@ -544,19 +513,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-// Row-major packed codes [rows][K/2] as a 2-D byte tensor; a box is
-// `box_rows` rows of 128 bytes (256 codes), 128-byte swizzle.
-bool encode_codes_map(CUtensorMap* map, const uint8_t* q, int64_t rows, int64_t K, int box_rows) {
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
-  const cuuint32_t box[2] = {kBKBytes, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(q), dims,
-                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // ---------------------------------------------------------------------------
 // Persistent variant (tiled scales): one CTA per SM walks the banded tile
 // order with four stages and a separate 16 KiB staging box, so the producer
@@ -891,46 +847,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
 // ---------------------------------------------------------------------------
 // CTA-pair kernel (tiled scales per 32): clusters of two CTAs walk the banded
-// order of 256 x 256 output tiles with tcgen05.mma.cta_group::2 (M = 256).
-// Each CTA loads its 128 rows of A and its 128 rows of B, so B costs each SM
-// half the bytes per flop of a one-CTA tile, plus the scales of its A rows
-// and of all 256 B rows (the MMA reads B's scales from each CTA's own TMEM).
-// The even CTA (rank 0) issues the scale copies, the MMAs and the commits;
-// the commits arrive on the barriers of both CTAs, and every TMA load of the
-// pair counts its bytes on rank 0's stage barrier.  No load uses cluster
-// multicast.  Every cross-CTA wait is bounded; both CTAs always reach the
-// final TMEM release.
-constexpr int kQBN = 128;                                     // B rows per CTA
-constexpr int kQBTile = kQBN * kBKBytes;                      // 16 KiB
-constexpr int kQStage = kATile + kQBTile + kSfaBytes + kSfbBytes;   // 35 KiB
+// order of 256 x 256 output tiles (the load and MMA roles are in kq_gemm.cuh).
+// Every cross-CTA wait is bounded; both CTAs always reach the final TMEM
+// release.
 constexpr int kQStages = 6;
+using QGeom = PairGeom<kBN, kQStages>;
 constexpr int kQBoxRows = 64;                                 // staging box: 64 rows x 128 B
 constexpr int kQStaging = kQBoxRows * 128;
-constexpr int kQSmem = 1024 + kQStages * kQStage + kQStaging + (2 * kQStages + 4) * 8 + 16;
-constexpr int kQTile = 2 * kBM;                               // 256 rows and columns a tile
-static_assert(kQStage % 1024 == 0, "stages keep the 1024-byte swizzle alignment");
+constexpr int kQSmem = 1024 + kQStages * QGeom::kStage + kQStaging + (2 * kQStages + 4) * 8 + 16;
 static_assert(kQSmem <= 232448, "shared memory");
-static_assert(kSfCol0 + kQStages * (kSfColsA + kSfColsB) <= kTmemCols, "TMEM columns");
-// M = 256 over the pair, N = 256.
-constexpr uint32_t kIdescMxf4Pair = (1u << 7) | (1u << 10) | (uint32_t(kBN >> 3) << 17) |
-                                    (1u << 23) | (uint32_t(kQTile >> 4) << 24);
-// Bytes one k-tile brings into the pair: codes of 128 A rows and 128 B rows,
-// the A scales of 128 rows and the B scales of 256 rows, per CTA.
-constexpr uint32_t kQTxBytes = 2u * kQStage;
 
 struct PairArgs {
-  int32_t K, k_tiles, m_tiles, n_tiles;     // tiles of 256 x 256
+  PairTiles tiles;
   int32_t out_bf16;
   int* err;
 };
-
-__device__ __forceinline__ void pair_tile_origin(const PairArgs& a, int t, int& m0, int& n0) {
-  const int band = t / (kBandN * a.m_tiles);
-  const int r = t - band * kBandN * a.m_tiles;
-  const int width = min(kBandN, a.n_tiles - band * kBandN);
-  m0 = (r / width) * kQTile;
-  n0 = (band * kBandN + r % width) * kQTile;
-}
 
 __global__ void __launch_bounds__(kPThreads, 1)
     gemm_mxf4_pair(const __grid_constant__ CUtensorMap amap,
@@ -940,7 +871,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                    const __grid_constant__ CUtensorMap cmap, const PairArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  uint8_t* staging = base + kQStages * kQStage;
+  uint8_t* staging = base + kQStages * QGeom::kStage;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kQStaging);
   uint64_t* empty = full + kQStages;
   uint64_t* acc_full = empty + kQStages;
@@ -949,8 +880,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
-  const int n_tiles_total = a.m_tiles * a.n_tiles;
-  const int nk = a.k_tiles;
+  const int n_tiles_total = a.tiles.m_tiles * a.tiles.n_tiles;
 
   if (tid == 0) {
     for (int st = 0; st < kQStages; ++st) {
@@ -968,99 +898,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      tma_prefetch_map(&amap);
-      tma_prefetch_map(&bmap);
-      tma_prefetch_map(&sfamap);
-      tma_prefetch_map(&sfbmap);
-      int s = 0, g = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int t = pair; t < n_tiles_total && ok; t += n_pairs) {
-        int m0, n0;
-        pair_tile_origin(a, t, m0, n0);
-        const int am0 = m0 + (int)rank * kBM, bn0 = n0 + (int)rank * kQBN;
-        for (int kt = 0; kt < nk; ++kt, ++g) {
-          if (g >= kQStages && !mbar_wait(&empty[s], phase)) {
-            ok = false;
-            break;
-          }
-          uint8_t* stg = base + s * kQStage;
-          const uint32_t fb = cluster_addr(&full[s], 0);
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], kQTxBytes);
-          uint8_t* sfa = stg + kATile + kQBTile;
-          // Scales: chunks 2 kt, 2 kt + 1 of this CTA's A row tile and of
-          // the tile's two B row tiles (zero past the ends).
-          tma_load_4d_pair(sfa, &sfamap, 0, 0, 2 * kt, am0 / 128, fb);
-          tma_load_4d_pair(sfa + kSfaBytes, &sfbmap, 0, 0, 2 * kt, n0 / 128, fb);
-          tma_load_2d_pair(stg, &amap, kt * kBKBytes, am0, fb);
-          tma_load_2d_pair(stg + kATile, &bmap, kt * kBKBytes, bn0, fb);
-          if (++s == kQStages) {
-            s = 0;
-            if (g >= kQStages) phase ^= 1;
-          }
-        }
-      }
-      if (!ok) atomicOr(a.err, kErrProducerWait);
-    }
+    if (lane == 0 && !pair_produce<kBN, kQStages>(base, full, empty, &amap, &bmap, &sfamap, &sfbmap,
+                                                  a.tiles, rank, pair, n_pairs))
+      atomicOr(a.err, kErrProducerWait);
   } else if (warp == 1) {
-    // -------------------------------------------------- scale copies + MMA
-    if (rank == 0 && lane == 0) {
-      int s = 0, i = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      auto ktile = [&](int kt, auto full_tile) -> bool {
-        if (!mbar_wait(&full[s], phase)) return false;
-        tmem_fence_after();
-        const uint8_t* stg = base + s * kQStage;
-        const uint8_t* sfa = stg + kATile + kQBTile;
-        const uint8_t* sfb = sfa + kSfaBytes;
-        const uint32_t tsfa = tmem_base + kSfCol0 + s * (kSfColsA + kSfColsB);
-        const uint32_t tsfb = tsfa + kSfColsA;
-#pragma unroll
-        for (int c = 0; c < kChunksPerStage; ++c) {
-          tmem_cp_pair_32x128b_x4(tsfa + 4 * c, smem_desc_rows16(smem_addr(sfa + c * kSfChunk)));
-#pragma unroll
-          for (int gb = 0; gb < kBN / 128; ++gb)
-            tmem_cp_pair_32x128b_x4(tsfb + 8 * c + 4 * gb,
-                                    smem_desc_rows16(smem_addr(sfb + (2 * gb + c) * kSfChunk)));
-        }
-        const uint64_t adesc = smem_desc_sw128(smem_addr(stg));
-        const uint64_t bdesc = smem_desc_sw128(smem_addr(stg + kATile));
-        const int n_mma = decltype(full_tile)::value
-                              ? kBK / kMmaK
-                              : min(kBK / kMmaK, (a.K - kt * kBK + kMmaK - 1) / kMmaK);
-#pragma unroll
-        for (int kk = 0; kk < kBK / kMmaK; ++kk) {
-          if (!decltype(full_tile)::value && kk >= n_mma) break;
-          const uint32_t sf_id = 2u * (kk & 1);
-          const uint32_t idesc = kIdescMxf4Pair | (sf_id << 29) | (sf_id << 4);
-          mma_mxf4_pair(tmem_base, adesc + 2 * kk, bdesc + 2 * kk, idesc, tsfa + 4 * (kk >> 1),
-                        tsfb + 8 * (kk >> 1), (kt | kk) != 0);
-        }
-        mma_commit_pair(&empty[s]);
-        if (++s == kQStages) {
-          s = 0;
-          phase ^= 1;
-        }
-        return true;
-      };
-      for (int t = pair; t < n_tiles_total && ok; t += n_pairs, ++i) {
-        // The accumulators are free once both CTAs' epilogues read tile i - 1.
-        if (i >= 1 && !mbar_wait_cluster(acc_empty, (i - 1) & 1)) {
-          ok = false;
-          break;
-        }
-        tmem_fence_after();
-        const int nk_full = a.K % kBK == 0 ? nk : nk - 1;
-        int kt = 0;
-        for (; ok && kt < nk_full; ++kt) ok = ktile(kt, std::true_type{});
-        if (ok && kt < nk) ok = ktile(kt, std::false_type{});
-        mma_commit_pair(acc_full);           // also after a failed wait: epilogues go on
-      }
-      if (!ok) atomicOr(a.err, kErrConsumerWait);
-    }
+    if (rank == 0 && lane == 0 &&
+        !pair_mma<kBN, kQStages>(base, full, empty, acc_full, acc_empty, tmem_base, a.tiles, pair,
+                                 n_pairs))
+      atomicOr(a.err, kErrConsumerWait);
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
@@ -1099,7 +944,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     int i = 0;
     for (int t = pair; t < n_tiles_total; t += n_pairs, ++i) {
       int m0, n0;
-      pair_tile_origin(a, t, m0, n0);
+      pair_tile_origin<kBN>(a.tiles, t, m0, n0);
       const int row0 = m0 + (int)rank * kBM;
       // One AND-barrier makes a timeout the same for the four warps, which
       // then stop (one bounded wait per failure, not one per tile).
@@ -1200,60 +1045,27 @@ bool pair_gemm() {
   return e ? atoi(e) != 0 : false;
 }
 
-// Tiled scales [row tiles][4-scale columns][512 bytes] as a 4-D byte tensor
-// {256, 2, columns, row tiles}; a box {256, 2, 2, box_tiles} is the two
-// columns of one k-tile for box_tiles row tiles (zeros past either end).
-bool encode_scales_map(CUtensorMap* map, const uint8_t* sf, int64_t row_tiles, int64_t cols,
-                       int box_tiles) {
-  const cuuint64_t dims[4] = {256, 2, static_cast<cuuint64_t>(cols),
-                              static_cast<cuuint64_t>(row_tiles)};
-  const cuuint64_t strides[3] = {256, 512, static_cast<cuuint64_t>(cols) * 512};
-  const cuuint32_t box[4] = {256, 2, 2, static_cast<cuuint32_t>(box_tiles)};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(sf),
-                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Launches the CTA-pair kernel: clusters of two, as many as can be resident.
 int launch_gemm_pair(const CUtensorMap& amap, const uint8_t* qb, const uint8_t* sa,
                      const uint8_t* sb, const CUtensorMap& cmap, const GemmArgs& g,
                      const DeviceInfo* di, int dev, cudaStream_t st) {
   CUtensorMap bmap, sfamap, sfbmap;
-  if (!encode_codes_map(&bmap, qb, g.N, g.K, kQBN) ||
+  if (!encode_codes_map(&bmap, qb, g.N, g.K, QGeom::kBRows) ||
       !encode_scales_map(&sfamap, sa, (g.M + 127) / 128, g.sf_tiles_k, 1) ||
-      !encode_scales_map(&sfbmap, sb, g.sf_tiles_n, g.sf_tiles_k, 2))
+      !encode_scales_map(&sfbmap, sb, g.sf_tiles_n, g.sf_tiles_k, QGeom::kGroups))
     return record_cuda_error(cudaErrorInvalidValue);
   PairArgs pa{};
-  pa.K = g.K;
-  pa.k_tiles = g.k_tiles;
-  pa.m_tiles = (g.M + kQTile - 1) / kQTile;
-  pa.n_tiles = (g.N + kQTile - 1) / kQTile;
+  pa.tiles.K = g.K;
+  pa.tiles.k_tiles = g.k_tiles;
+  pa.tiles.m_tiles = (g.M + kPairM - 1) / kPairM;
+  pa.tiles.n_tiles = (g.N + kBN - 1) / kBN;
   pa.out_bf16 = g.out_bf16;
   pa.err = g.err;
   int rc = allow_smem<gemm_mxf4_pair>(kQSmem, dev);
   if (rc != KQ_OK) return rc;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.blockDim = dim3(kPThreads);
-  cfg.dynamicSmemBytes = kQSmem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (di->sms / 2)));
-  int clusters = 0;
-  cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters, gemm_mxf4_pair, &cfg);
-  if (e != cudaSuccess || clusters < 1) return record_cuda_error(e != cudaSuccess ? e : cudaErrorInvalidConfiguration);
-  const int64_t tiles = (int64_t)pa.m_tiles * pa.n_tiles;
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(tiles, clusters)));
-  e = cudaLaunchKernelEx(&cfg, gemm_mxf4_pair, amap, bmap, sfamap, sfbmap, cmap, pa);
-  if (e != cudaSuccess) return record_cuda_error(e);
-  return KQ_OK;
+  return launch_pairs<gemm_mxf4_pair>(kPThreads, kQSmem,
+                                      (int64_t)pa.tiles.m_tiles * pa.tiles.n_tiles, di, dev, false,
+                                      st, amap, bmap, sfamap, sfbmap, cmap, pa);
 }
 
 int launch_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const uint8_t* sb,

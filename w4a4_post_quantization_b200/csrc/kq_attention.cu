@@ -12,42 +12,10 @@
 #include <algorithm>
 #include <cmath>
 
-#include "kq_cache.cuh"
-#include "kq_internal.h"
+#include "kq_attention.cuh"
 
 namespace kq {
 namespace {
-
-constexpr float kLn2 = 0.6931471805599453f;
-
-struct AttnArgs {
-  CacheView view;
-  const uint8_t *kc, *ks, *vc, *vs;
-  const uint16_t* q;
-  uint16_t* out;
-  float* lse;                      // [batch][heads][M], or null
-  const int32_t* lens;
-  int64_t qb, qm, qh, ob, om, oh;  // strides in elements
-  int32_t M, D, max_len;
-  int32_t rows;                    // query rows of one K/V head: group * M
-  int32_t causal;
-  FastDiv group;                   // query heads per K/V head
-  float scale_log2;                // scale * log2(e)
-  int32_t chunk, n_chunks;         // positions per CTA, CTAs along the positions
-  float* part_o;                   // [batch][K/V head][chunk][row][Dp]
-  float2* part_ml;                 // (maximum, sum) of the same
-  int* err;
-};
-
-// Row r of a K/V head is query m = r / group of head group * hk + r % group.
-__device__ __forceinline__ int seq_len(const AttnArgs& a, int64_t b) {
-  return max(0, min(a.lens[b], a.max_len));
-}
-// Positions row r sees: [0, row_limit).
-__device__ __forceinline__ int row_limit(const AttnArgs& a, int len, int r) {
-  if (r >= a.rows) return 0;
-  return a.causal ? max(0, len - a.M + static_cast<int>(a.group.div(r)) + 1) : len;
-}
 
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
@@ -58,23 +26,6 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -83,29 +34,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
-// Four pairs of codes out of a word: pair i is nibble i of the low half and
-// nibble i of the high half, as bf16 bits.  A code's sign goes to bit 15 and
-// its exponent and mantissa (two bits and one) to bits 8..6, the low end of
-// bf16's fields, where they mean the code's value times 2^-126: the exponent
-// 0 of E2M1 is bf16's own subnormal.  mx_pair puts the factor right together
-// with the block's scale.
-__device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&p)[4]) {
-  p[0] = ((w << 6) & 0x01C001C0u) | ((w << 12) & 0x80008000u);
-  p[1] = ((w << 2) & 0x01C001C0u) | ((w << 8) & 0x80008000u);
-  p[2] = ((w >> 2) & 0x01C001C0u) | ((w << 4) & 0x80008000u);
-  p[3] = ((w >> 6) & 0x01C001C0u) | (w & 0x80008000u);
-}
-
-// bf16 bits of 2^(s - 63) for scale byte s <= 190: a raw code times it is the
-// value times 2^-62, exactly (2^-126 of the raw bits, 2^(s - 127) of the
-// scale).  The 2^62 keeps the multiplier in bf16's range for every scale byte
-// up to 190 (values below 2^66).  It is undone in the scores' scale, and in the
-// softmax weights, which are held as 2^62 exp2(.): their products with V then
-// have V's own range, so small weights are not lost to underflow.
-__device__ __forceinline__ uint32_t mx_mul(uint32_t s) { return (s + 64) << 7; }
-constexpr int kShift = 62;
-constexpr float kUnscale = 4611686018427387904.0f;      // 2^kShift
 
 // ---------------------------------------------------------------------------
 // Few query rows: one warp walks 32 positions at a time with mma.sync, its
@@ -511,36 +439,45 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int64_
         top == -INFINITY ? -INFINITY : (top + (log2f(sum) - kShift)) * kLn2;
 }
 
-// How a call is cut: from its sizes alone, so that the workspace query and the
-// call agree.
-struct Plan {
-  int row_groups, mt;
-  int64_t chunk, n_chunks;
-  size_t ml_bytes, bytes;
-};
-
-Plan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int nb) {
-  Plan p{};
-  p.mt = rows > 16 ? 2 : 1;
-  p.row_groups = static_cast<int>((rows + 16 * p.mt - 1) / (16 * p.mt));
-  constexpr int64_t kStep = kTile * kWarps;
-  // About eight CTAs for each of the 148 SMs, of at least 512 positions.
-  const int64_t units = batch * kv_heads * p.row_groups;
-  const int64_t want = std::max<int64_t>(1, 8 * 148 / units);
-  int64_t chunk = std::max<int64_t>(512, (max_len + want - 1) / want);
-  chunk = (chunk + kStep - 1) / kStep * kStep;
-  p.chunk = chunk;
-  p.n_chunks = std::max<int64_t>(1, (max_len + chunk - 1) / chunk);
+AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int64_t head_dim) {
+  AttnPlan p{};
+  constexpr int64_t kSms = 148;
+  const int64_t nb = (head_dim + 31) / 32, d16 = (head_dim + 15) / 16 * 16;
+  p.tiles = (max_len + 127) / 128;
+  const int64_t images = batch * kv_heads * p.tiles * 512 * d16;
+  p.tensor_core = rows > 32 && images <= (int64_t(1) << 32);
+  if (p.tensor_core) {
+    p.q_tiles = 2;
+    const int64_t units = batch * kv_heads * ((rows + 255) / 256);
+    // Cut along the positions where there are too few CTAs, into parts of at
+    // least four tiles.
+    const int64_t want = std::max<int64_t>(1, std::min(kSms / units, (p.tiles + 3) / 4));
+    p.chunk = (p.tiles + want - 1) / want * 128;
+    p.mask_bytes = static_cast<size_t>((batch * p.tiles * 16 + 255) / 256 * 256);
+    p.image_bytes = static_cast<size_t>(images);
+  } else {
+    p.mt = rows > 16 ? 2 : 1;
+    p.row_groups = static_cast<int>((rows + 16 * p.mt - 1) / (16 * p.mt));
+    constexpr int64_t kStep = kTile * kWarps;
+    // About eight CTAs for each SM, of at least 512 positions.
+    const int64_t units = batch * kv_heads * p.row_groups;
+    const int64_t want = std::max<int64_t>(1, 8 * kSms / units);
+    const int64_t chunk = std::max<int64_t>(512, (max_len + want - 1) / want);
+    p.chunk = (chunk + kStep - 1) / kStep * kStep;
+  }
+  p.n_chunks = std::max<int64_t>(1, (max_len + p.chunk - 1) / p.chunk);
   if (p.n_chunks > 1) {
     const int64_t parts = batch * kv_heads * p.n_chunks * rows;
     p.ml_bytes = static_cast<size_t>((parts * 8 + 255) / 256 * 256);
-    p.bytes = p.ml_bytes + static_cast<size_t>(parts) * nb * 32 * 4;
+    p.part_bytes = static_cast<size_t>(parts) * nb * 32 * 4;
+    p.part_bytes = (p.part_bytes + 255) / 256 * 256;
   }
+  p.bytes = p.ml_bytes + p.part_bytes + p.mask_bytes + p.image_bytes;
   return p;
 }
 
 template <int kW, int kMT>
-int launch_split(const AttnArgs& a, const Plan& p, int64_t batch, int dev, cudaStream_t st) {
+int launch_split(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
   constexpr int smem = split_smem<kW, kMT>();
   const int rc = allow_smem<attn_split_kernel<kW, kMT>>(smem, dev);
   if (rc != KQ_OK) return rc;
@@ -548,18 +485,19 @@ int launch_split(const AttnArgs& a, const Plan& p, int64_t batch, int dev, cudaS
                   static_cast<unsigned>(a.view.heads), static_cast<unsigned>(batch));
   cudaError_t e = launch_pdl(attn_split_kernel<kW, kMT>, grid, dim3(32 * kWarps), smem, st, a);
   if (e != cudaSuccess) return record_cuda_error(e);
-  if (a.n_chunks > 1) {
-    const int64_t n_rows = batch * a.view.heads * a.rows;
-    e = launch_pdl(attn_join_kernel<kW>, dim3(static_cast<unsigned>((n_rows + 3) / 4)), dim3(128), 0,
-                   st, a, n_rows);
-    if (e != cudaSuccess) return record_cuda_error(e);
-  }
   return KQ_OK;
 }
 
 template <int kW>
-int launch_split_mt(const AttnArgs& a, const Plan& p, int64_t batch, int dev, cudaStream_t st) {
-  return p.mt == 1 ? launch_split<kW, 1>(a, p, batch, dev, st) : launch_split<kW, 2>(a, p, batch, dev, st);
+int launch(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
+  const int rc = p.tensor_core ? launch_attention_tc(a, p, batch, dev, st)
+                 : p.mt == 1   ? launch_split<kW, 1>(a, p, batch, dev, st)
+                               : launch_split<kW, 2>(a, p, batch, dev, st);
+  if (rc != KQ_OK || p.n_chunks == 1) return rc;
+  const int64_t n_rows = batch * a.view.heads * a.rows;
+  const cudaError_t e = launch_pdl(attn_join_kernel<kW>, dim3(static_cast<unsigned>((n_rows + 3) / 4)),
+                                   dim3(128), 0, st, a, n_rows);
+  return e == cudaSuccess ? KQ_OK : record_cuda_error(e);
 }
 
 // Sizes a call can have: 0 where they are not valid, else the rows of a K/V
@@ -584,7 +522,7 @@ extern "C" size_t kq_attention_workspace_bytes(int64_t batch, int64_t M, int64_t
                                                int64_t kv_heads, int64_t head_dim, int64_t max_len) {
   const int64_t rows = attention_rows(batch, M, heads, kv_heads, head_dim, max_len);
   if (rows == 0) return 0;
-  return make_plan(batch, kv_heads, rows, max_len, static_cast<int>((head_dim + 31) / 32)).bytes;
+  return make_plan(batch, kv_heads, rows, max_len, head_dim).bytes;
 }
 
 extern "C" int kq_attention_mxfp4(const uint16_t* q, int64_t q_sb, int64_t q_sm, int64_t q_sh,
@@ -607,9 +545,8 @@ extern "C" int kq_attention_mxfp4(const uint16_t* q, int64_t q_sb, int64_t q_sm,
   if (!al(q, 16) || !al(out, 16) || !al(lens, 4) || !strides(q_sb, q_sm, q_sh) ||
       !strides(o_sb, o_sm, o_sh) || (lse && !al(lse, 4)) || !std::isfinite(scale))
     return KQ_ERR_INVALID;
-  const Plan p = make_plan(batch, cache->heads, rows, max_len, a.view.nb);
+  const AttnPlan p = make_plan(batch, cache->heads, rows, max_len, cache->head_dim);
   if (p.bytes > 0 && (!al(workspace, 256) || workspace_bytes < p.bytes)) return KQ_ERR_INVALID;
-  if (p.n_chunks * p.row_groups >= (int64_t(1) << 31)) return KQ_ERR_INVALID;
   const DeviceInfo* di = nullptr;
   int dev = 0;
   int rc = device_info(&di, &dev);
@@ -630,13 +567,18 @@ extern "C" int kq_attention_mxfp4(const uint16_t* q, int64_t q_sb, int64_t q_sm,
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.chunk = static_cast<int32_t>(p.chunk);
   a.n_chunks = static_cast<int32_t>(p.n_chunks);
-  a.part_ml = static_cast<float2*>(workspace);
-  a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.ml_bytes);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.part_ml = reinterpret_cast<float2*>(ws);
+  a.part_o = reinterpret_cast<float*>(ws + p.ml_bytes);
+  a.tile_mask = reinterpret_cast<const uint4*>(ws + p.ml_bytes + p.part_bytes);
+  a.images = ws + p.ml_bytes + p.part_bytes + p.mask_bytes;
+  a.tiles = static_cast<int32_t>(p.tiles);
+  a.d16 = static_cast<int32_t>((cache->head_dim + 15) / 16 * 16);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (a.view.nb) {
-    case 1: return launch_split_mt<1>(a, p, batch, dev, st);
-    case 2: return launch_split_mt<2>(a, p, batch, dev, st);
-    case 3: return launch_split_mt<3>(a, p, batch, dev, st);
-    default: return launch_split_mt<4>(a, p, batch, dev, st);
+    case 1: return launch<1>(a, p, batch, dev, st);
+    case 2: return launch<2>(a, p, batch, dev, st);
+    case 3: return launch<3>(a, p, batch, dev, st);
+    default: return launch<4>(a, p, batch, dev, st);
   }
 }

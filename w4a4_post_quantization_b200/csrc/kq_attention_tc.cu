@@ -2,19 +2,22 @@
 //
 // Every 128-row tile of queries multiplies the same keys and values, so they
 // are decoded once per call, by a first kernel, into tiles of 128 positions laid
-// out as the MMA reads them:
-//   K image  [channel / 16][position][16 channels]   (K-major B operand of S = Q K^T)
-//   V image  [position / 16][channel][16 positions]  (K-major B operand of O = P V)
-// in bf16, both in 32-byte rows with the 32-byte swizzle, so a head of any
-// multiple of 16 channels takes no padding beyond that, and a tile arrives as one
-// plain bulk copy of 256 D bytes.
+// out as the MMA reads them, in bf16:
+//   K image  [channel panel][position][channels of the panel]   (B of S = Q K^T)
+//   V image  [position / 64][channel][64 positions]             (B of O = P V)
+// both K-major.  V's rows are 128 bytes with the 128-byte swizzle.  K's channels
+// (a multiple of 16) are cut into panels of 64, then one of 32 and one of 16
+// for the rest, each with the swizzle of its row, so that a head of 72 or 112
+// channels takes no padding beyond 16 and a tile arrives as one plain bulk copy of
+// 256 D bytes.  (Panels of 16 throughout, with the 32-byte swizzle, made the
+// operand reads the bound: 2048 x 8192 causal, 32 heads of 128, took 295 us.)
 //
 // The second kernel gives a CTA kQT tiles of 128 rows (query, head of the group)
 // of one K/V head.  Warps 0 .. 4 kQT - 1 hold one row a thread: scores out of
 // tensor memory, the running maximum and sum, weights back into it as bf16 in
 // the scores' place, where the second product reads them.  One thread loads and
 // one issues the MMAs; with two query tiles the products of one run under the
-// softmax of the other.  The accumulator O stays in tensor memory.  It is
+// softmax of the other (a warp issues for each).  The accumulator O stays in tensor memory.  It is
 // rescaled only when a row's maximum has grown by more than 2^8: until then the
 // weights are relative to the older maximum, which float32 and bf16 hold as
 // well.
@@ -30,17 +33,44 @@ namespace {
 constexpr int kKv = 128;                       // positions of a tile
 constexpr int kQr = 128;                       // rows of a query tile
 
-// K-major operand in 32-byte rows, 32-byte swizzle: 8-row atoms of 256 bytes;
-// 16-byte chunk c of row r lies at c ^ (r / 4 mod 2).
+// K-major operand in 32-byte rows, 32-byte swizzle: 8-row atoms of 256 bytes.
 __device__ __forceinline__ uint64_t smem_desc_sw32(uint32_t saddr) {
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) |
          (uint64_t(256 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(6) << 61);
 }
 
+// Channel panels of 128 rows (Q and K): byte offset of 16-byte chunk c (8
+// channels) of row r.  A swizzle moves chunk c of a row of n chunks to
+// c ^ (bits 3.. of the row's 128-byte line).
+__device__ __forceinline__ int panel_chunk(int d16, int r, int c) {
+  const int wide = d16 >> 6;
+  if (c < 8 * wide) return (c >> 3) * 16384 + r * 128 + 16 * ((c & 7) ^ (r & 7));
+  c -= 8 * wide;
+  if (d16 & 32) {
+    if (c < 4) return wide * 16384 + r * 64 + 16 * (c ^ ((r >> 1) & 3));
+    c -= 4;
+  }
+  return wide * 16384 + (d16 & 32) * 256 + r * 32 + 16 * (c ^ ((r >> 2) & 1));
+}
+// Descriptor of K step k (16 channels) of such a tile at a 1024-byte-aligned
+// address.  The head's width is a template argument where MMAs are issued: the
+// one issuing thread bounds the kernel if it has to work the descriptors out.
+template <int kD16>
+__device__ __forceinline__ uint64_t panel_desc(uint32_t saddr, int k) {
+  constexpr int kWide = kD16 >> 6;
+  if (k < 4 * kWide) return smem_desc_sw128(saddr) + ((k >> 2) * 16384 + (k & 3) * 32) / 16;
+  if ((kD16 & 32) && k < 4 * kWide + 2)
+    return smem_desc_sw64(saddr) + (kWide * 16384 + (k - 4 * kWide) * 32) / 16;
+  return smem_desc_sw32(saddr) + (kWide * 16384 + (kD16 & 32) * 256) / 16;
+}
+
 // ------------------------------------------------------------------ decode
 constexpr int kDecodeThreads = 256;
 
-// One tile of one K/V head of one sequence: K by blockIdx.z even, V odd.
+// One tile of one K/V head of one sequence: K for even blockIdx.y, V for odd.
+// The tile's codes and scales are staged in shared memory by 16-byte loads, all
+// in flight together, so that the decoding reads them in whatever order makes
+// the stores whole 128-byte lines.
 __global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(const AttnArgs a, uint4* masks,
                                                                      uint8_t* images) {
   pdl_wait_then_trigger();
@@ -50,67 +80,80 @@ __global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(const AttnA
   const int len = seq_len(a, b);
   const int pos0 = tile * kKv;
   if (pos0 >= len) return;
-  __shared__ int64_t rows[kKv];                // cache row of each position, -1: none
-  if (tid < kKv) {
-    const int64_t r = pos0 + tid < len ? cache_row(a.view, b, pos0 + tid, hk) : -1;
+  const int nb = a.view.nb;
+  __shared__ int64_t rows[kKv / 16];           // cache row of each 16 positions, -1: none
+  __shared__ uint32_t there[kKv / 32];         // which positions there are
+  __shared__ __align__(16) uint8_t codes[kKv * 64];
+  __shared__ __align__(16) uint8_t scales[kKv * 4];
+  if (tid < kKv / 16) {
+    const int pos = pos0 + 16 * tid;
+    const int64_t r = pos < len ? cache_row(a.view, b, pos, hk) : -1;
     rows[tid] = r;
-    const bool there = r >= 0;
-    const uint32_t bits = __ballot_sync(0xFFFFFFFFu, there);
-    if (!there && pos0 + tid < len) atomicOr(a.err, kErrCacheIndex);
-    if (hk == 0 && !is_v && (tid & 31) == 0)
-      reinterpret_cast<uint32_t*>(masks + b * a.tiles + tile)[tid >> 5] = bits;
+    if (r < 0 && pos < len) atomicOr(a.err, kErrCacheIndex);
+  }
+  __syncthreads();
+  if (tid < kKv / 32) {
+    uint32_t bits = (rows[2 * tid] >= 0 ? 0xFFFFu : 0u) | (rows[2 * tid + 1] >= 0 ? 0xFFFF0000u : 0u);
+    const int left = len - pos0 - 32 * tid;
+    if (left < 32) bits &= left <= 0 ? 0u : (1u << left) - 1u;
+    there[tid] = bits;
+    if (hk == 0 && !is_v) reinterpret_cast<uint32_t*>(masks + b * a.tiles + tile)[tid] = bits;
+  }
+  // 16 positions are 16 nb 16-byte pieces of codes and nb of scales in a row.
+  const uint8_t* gc = is_v ? a.vc : a.kc;
+  const uint8_t* gs = is_v ? a.vs : a.ks;
+  for (int i = tid; i < kKv * nb; i += kDecodeThreads) {
+    const int64_t r = rows[i / (16 * nb)];
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r >= 0) x = __ldg(reinterpret_cast<const uint4*>(gc + r * (16 * nb)) + i % (16 * nb));
+    reinterpret_cast<uint4*>(codes)[i] = x;
+  }
+  if (tid < kKv / 16 * nb) {
+    const int64_t r = rows[tid / nb];
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r >= 0) x = __ldg(reinterpret_cast<const uint4*>(gs + r * nb) + tid % nb);
+    reinterpret_cast<uint4*>(scales)[tid] = x;
   }
   __syncthreads();
   uint8_t* img = images + (((b * a.view.heads + hk) * a.tiles + tile) * 2 + is_v) * (256 * a.d16);
-  const int nb = a.view.nb;
   if (!is_v) {
-    // Item: 16 channels of a position.
-    for (int i = tid; i < (a.d16 / 16) * kKv; i += kDecodeThreads) {
-      const int p = i >> 7, t = i & 127;
-      const int64_t r = rows[t];
+    // Item: 16 channels of a position; a row's panels to neighbouring lanes.
+    const int np = a.d16 / 16;
+    for (int i = tid; i < np * kKv; i += kDecodeThreads) {
+      const int t = i / np, p = i - t * np;
+      const uint2 w = *reinterpret_cast<const uint2*>(codes + t * (16 * nb) + 8 * p);
+      const bool in = there[t >> 5] >> (t & 31) & 1;
+      const uint32_t m = in ? mx_mul(scales[t * nb + (p >> 1)]) * 0x10001u : 0u;
       uint32_t o[8];
+      // A word's channels come out as the pairs (k, k + 4): put back in order.
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = 0;
-      if (r >= 0) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.kc + r * (16 * nb)) + p);
-        const uint32_t m = mx_mul(__ldg(a.ks + r * nb + (p >> 1))) * 0x10001u;
-        // Channels 0..3 and 4..7 of a word come out as the pairs (k, k + 4):
-        // put back in order.
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[4];
+        e2m1_pairs(h ? w.y : w.x, x);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[4];
-          e2m1_pairs(h ? w.y : w.x, x);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = mul_bf16x2(x[k], m);
-          o[4 * h] = __byte_perm(x[0], x[1], 0x5410);
-          o[4 * h + 1] = __byte_perm(x[2], x[3], 0x5410);
-          o[4 * h + 2] = __byte_perm(x[0], x[1], 0x7632);
-          o[4 * h + 3] = __byte_perm(x[2], x[3], 0x7632);
-        }
+        for (int k = 0; k < 4; ++k) x[k] = mul_bf16x2(x[k], m);
+        o[4 * h] = __byte_perm(x[0], x[1], 0x5410);
+        o[4 * h + 1] = __byte_perm(x[2], x[3], 0x5410);
+        o[4 * h + 2] = __byte_perm(x[0], x[1], 0x7632);
+        o[4 * h + 3] = __byte_perm(x[2], x[3], 0x7632);
       }
-      uint8_t* dst = img + p * (kKv * 32) + t * 32;
-      const int sw = (t >> 2) & 1;
-      *reinterpret_cast<uint4*>(dst + 16 * sw) = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4*>(dst + 16 * (1 - sw)) = make_uint4(o[4], o[5], o[6], o[7]);
+      *reinterpret_cast<uint4*>(img + panel_chunk(a.d16, t, 2 * p)) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(img + panel_chunk(a.d16, t, 2 * p + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
     }
   } else {
-    // Item: 8 channels of 16 positions, transposed pair by pair.
-    const int words = a.d16 / 8;
-    for (int i = tid; i < words * (kKv / 16); i += kDecodeThreads) {
-      const int p = i / words, wd = i - p * words;
-      uint32_t o[8][8];                        // [channel][pair of positions]
+    // Item: 8 channels of 8 positions, transposed pair by pair; the positions of
+    // a channel to neighbouring lanes.
+    for (int i = tid; i < a.d16 / 8 * (kKv / 8); i += kDecodeThreads) {
+      const int p = i & 15, wd = i >> 4;
+      const uint32_t in = there[p >> 2] >> (8 * (p & 3));
+      uint32_t o[8][4];                        // [channel][pair of positions]
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int64_t r0 = rows[16 * p + 2 * k], r1 = rows[16 * p + 2 * k + 1];
-        uint32_t w0 = 0, w1 = 0, m = 0;
-        if (r0 >= 0) {
-          w0 = __ldg(reinterpret_cast<const uint32_t*>(a.vc + r0 * (16 * nb)) + wd);
-          m = mx_mul(__ldg(a.vs + r0 * nb + (wd >> 2)));
-        }
-        if (r1 >= 0) {
-          w1 = __ldg(reinterpret_cast<const uint32_t*>(a.vc + r1 * (16 * nb)) + wd);
-          m |= mx_mul(__ldg(a.vs + r1 * nb + (wd >> 2))) << 16;
-        }
+      for (int k = 0; k < 4; ++k) {
+        const int t = 8 * p + 2 * k;
+        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(codes + t * (16 * nb) + 4 * wd);
+        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(codes + (t + 1) * (16 * nb) + 4 * wd);
+        const uint32_t m = (in >> (2 * k) & 1 ? mx_mul(scales[t * nb + (wd >> 2)]) : 0u) |
+                           (in >> (2 * k + 1) & 1 ? mx_mul(scales[(t + 1) * nb + (wd >> 2)]) << 16 : 0u);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t x[4];
@@ -121,16 +164,22 @@ __global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(const AttnA
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int d = 8 * wd + e, sw = (d >> 2) & 1;
-        uint8_t* dst = img + p * (a.d16 * 32) + d * 32;
-        *reinterpret_cast<uint4*>(dst + 16 * sw) = make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]);
-        *reinterpret_cast<uint4*>(dst + 16 * (1 - sw)) = make_uint4(o[e][4], o[e][5], o[e][6], o[e][7]);
+        const int d = 8 * wd + e;
+        *reinterpret_cast<uint4*>(img + (p >> 3) * (a.d16 * 128) + d * 128 + 16 * ((p & 7) ^ (d & 7))) =
+            make_uint4(o[e][0], o[e][1], o[e][2], o[e][3]);
       }
     }
   }
 }
 
 // --------------------------------------------------------------- attention
+// The whole warp runs the loop that issues the MMAs, in uniform control flow,
+// and an elected lane issues each batch of them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t acc) {
   asm volatile(
@@ -179,27 +228,213 @@ __device__ __forceinline__ void bulk_load_1d(void* dst, const void* src, uint32_
 }
 
 // D float32, A and B bf16, both K-major, M = 128.
-__device__ __forceinline__ uint32_t idesc_bf16(int n) {
+__host__ __device__ constexpr uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(kQr >> 4) << 24);
 }
 
-template <int kQT>
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+template <int kQT, int kD16>
 struct TcGeom {
-  static constexpr int kStages = kQT == 2 ? 2 : 1;
-  static constexpr int kThreads = 128 * kQT + 64;
+  // Two blocks of one query tile share an SM: 113 KB each.
+  static constexpr int kStages = kQT == 2 || kD16 <= 80 ? 2 : 1;
+  // Softmax warpgroups, and one whose first two warps load and issue the MMAs
+  // (its registers go to the others: (kQT kSoftRegs + kRestRegs) is within
+  // what (kQT + 1) warpgroups are launched with).
+  static constexpr int kThreads = 128 * (kQT + 1);
+  static constexpr int kSoftRegs = kQT == 2 ? 208 : 200;
+  static constexpr int kRestRegs = kQT == 2 ? 80 : 56;
   static constexpr int kTmem = 256 * kQT;      // S (128 columns), then O (up to 128), per query tile
   // Q tiles, K and V stages, barriers.
-  static constexpr int smem(int d16) { return 1024 + (kQT + 2 * kStages) * 256 * d16 + 256; }
+  static constexpr int kSmem = 1024 + (kQT + 2 * kStages) * 256 * kD16 + 256;
+  static_assert(kSmem <= (kQT == 2 ? 232448 : 115712), "shared memory");
 };
 
+// 2^y for both halves without the special-function unit, for y >= -126: 2^f of
+// the fraction by the polynomial of degree 4 with the least relative error over
+// [-1/2, 1/2] (2.6e-6, by Remez' exchange), the integer into the exponent.
+__device__ __forceinline__ void ex2_poly(f2 y, float& p0, float& p1) {
+  const f2 magic = pack2(12582912.0f, 12582912.0f);         // 1.5 2^23: rounds to an integer
+  const f2 r = add2(y, magic);
+  const f2 f = sub2(y, sub2(r, magic));
+  f2 q = fma2(f, pack2(0.009570102207362652f, 0.009570102207362652f),
+              pack2(0.05591785907745361f, 0.05591785907745361f));
+  q = fma2(q, f, pack2(0.240247443318367f, 0.240247443318367f));
+  q = fma2(q, f, pack2(0.6931217908859253f, 0.6931217908859253f));
+  q = fma2(q, f, pack2(0.9999992847442627f, 0.9999992847442627f));
+  float r0, r1, q0, q1;
+  unpack2(r, r0, r1);
+  unpack2(q, q0, q1);
+  p0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(r0) << 23));
+  p1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(r1) << 23));
+}
+
+// mbar_wait as one tight loop, for the waits on every tile's critical path; each
+// poll suspends the warp for a time that the hardware bounds.
+__device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+      "POLL:\n\t"
+      "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 1000;\n\t@q bra POLL;\n"
+      "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done ? true : mbar_wait(bar, parity);
+}
+
+// Every so many pairs of weights of a whole tile take ex2_poly, the others the
+// special-function unit, which alone would need 8 cycles for each of a warp's 128
+// columns.  2048 x 8192 causal, 32 heads of 128: every 2nd 234 us, 3rd 244, 4th
+// 249, none 256; with one query tile a block, which shares the issue slots
+// with another block, 253, 243, 240 and 263.
 template <int kQT>
-__global__ void __launch_bounds__(TcGeom<kQT>::kThreads, kQT == 2 ? 1 : 2)
+constexpr int kPolyEvery = kQT == 2 ? 2 : 4;
+
+// With two query tiles the warps of the two that share a scheduler take turns at
+// the exponentials: while one is at them, the other's products run.  Left alone,
+// both come to wait for their scores at the same time.  Each call of my_turn on one
+// side needs a next_turn on the other; the first turn is tile 0's.
+template <int kQT>
+__device__ __forceinline__ void my_turn(int warp) {
+  if constexpr (kQT == 2) asm volatile("bar.sync %0, 64;" ::"r"(1 + warp) : "memory");
+}
+template <int kQT>
+__device__ __forceinline__ void next_turn(int warp) {
+  if constexpr (kQT == 2) asm volatile("bar.arrive %0, 64;" ::"r"(1 + (warp ^ 4)) : "memory");
+}
+
+// -inf for the positions a row does not see.
+__device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t see) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(see >> e & 1)) x[e] = 0xFF800000u;
+}
+
+// This warp's stores of weights so far are in tensor memory.  The second product
+// starts on the first half of a tile's weights.
+__device__ __forceinline__ void weights_ready(uint64_t* bar, int lane) {
+  tmem_wait_st();
+  tmem_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// A row's 128 scores to weights.  kWhole: the row sees every position; else
+// `see` says which, `words` of 32 of them are looked at, and the others' weights
+// are not used.
+template <bool kWhole, int kD16, int kQT>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sc, float& mx, float& l,
+                                             bool first, const uint32_t (&see)[4], int words,
+                                             uint64_t* p_half, int warp, int lane,
+                                             bool last_turn) {
+  // The maximum of words 2 and 3 is taken first and they are read again later,
+  // so that 64 scores at a time are in registers.
+  uint32_t x[2][32];
+  float peak = -INFINITY;
+#pragma unroll
+  for (int h = 1; h >= 0; --h) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (kWhole || 2 * h + u < words) tmem_ld32(ts + 32 * (2 * h + u), x[u]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int v = 2 * h + u;
+      if (!kWhole && v >= words) continue;
+      if (!kWhole) hide(x[u], see[v]);
+      float top[2] = {__uint_as_float(x[u][0]), __uint_as_float(x[u][1])};
+#pragma unroll
+      for (int e = 2; e < 30; e += 4) {
+        top[0] = max3(top[0], __uint_as_float(x[u][e]), __uint_as_float(x[u][e + 1]));
+        top[1] = max3(top[1], __uint_as_float(x[u][e + 2]), __uint_as_float(x[u][e + 3]));
+      }
+      peak = max3(peak, top[0], max3(top[1], __uint_as_float(x[u][30]), __uint_as_float(x[u][31])));
+    }
+  }
+  const float peak2 = peak * sc;
+  if (__any_sync(0xFFFFFFFFu, peak2 > mx + 8.0f)) {
+    const float m_new = fmaxf(mx, peak2);
+    const float alpha = m_new == -INFINITY ? 1.0f : ex2(mx - m_new);
+    mx = m_new;
+    l *= alpha;
+    // These scores were issued after the last weights' product, so O is
+    // complete.
+    if (!first) {
+#pragma unroll 1
+      for (int c = 0; c < kD16 / 16; ++c) {
+        uint32_t o[16];
+        tmem_ld16(to + 16 * c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+        tmem_st16(to + 16 * c, o);
+      }
+    }
+  }
+  my_turn<kQT>(warp);
+  const float shift = kShift - (mx == -INFINITY ? 0.0f : mx);
+  const f2 sc2 = pack2(sc, sc), shift2 = pack2(shift, shift);
+  f2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int u = v & 1;
+    if (kWhole || v < words) {
+      if (v >= 2) {
+        if (v == 2) tmem_wait_ld();
+        if (!kWhole) hide(x[u], see[v]);
+      }
+      uint32_t p[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const f2 y = fma2(pack2(__uint_as_float(x[u][2 * e]), __uint_as_float(x[u][2 * e + 1])), sc2,
+                          shift2);
+        float p0, p1;
+        unpack2(y, p0, p1);
+        if (kWhole && e % kPolyEvery<kQT> == kPolyEvery<kQT> - 1) {
+          ex2_poly(pack2(fmaxf(p0, -126.0f), fmaxf(p1, -126.0f)), p0, p1);
+        } else {
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+        }
+        sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
+        // Rounded to bf16, the type of the product; the sum is taken before.
+        p[e] = bf16x2(p0, p1);
+      }
+      // The weights of word v lie in the first half of the scores' columns,
+      // which have all been read.
+      if (v == 2) weights_ready(p_half, lane);              // words 0 and 1, stored a while ago
+      tmem_st16(ts + 16 * v, p);
+    } else if (v == 2) {
+      weights_ready(p_half, lane);
+    }
+    if (v < 2 && (kWhole || v + 2 < words)) tmem_ld32(ts + 32 * (v + 2), x[u]);
+  }
+  if (!last_turn) next_turn<kQT>(warp);
+  weights_ready(p_half + 1, lane);
+  float s0, s1;
+  unpack2(add2(sum[0], sum[1]), s0, s1);
+  l += s0 + s1;
+}
+
+template <int kQT, int kD16>
+__global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
     attn_tc_kernel(const AttnArgs a) {
-  using G = TcGeom<kQT>;
+  using G = TcGeom<kQT, kD16>;
   constexpr int kStages = G::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-  const int d16 = a.d16, img = 256 * d16;
+  constexpr int d16 = kD16, img = 256 * d16;
   uint8_t* sq = base;
   uint8_t* sk = sq + kQT * img;
   uint8_t* sv = sk + kStages * img;
@@ -208,10 +443,10 @@ __global__ void __launch_bounds__(TcGeom<kQT>::kThreads, kQT == 2 ? 1 : 2)
   uint64_t* v_full = k_empty + kStages;
   uint64_t* v_empty = v_full + kStages;
   uint64_t* q_full = v_empty + kStages;
-  uint64_t* s_full = q_full + 1;
-  uint64_t* p_full = s_full + kQT;
-  uint64_t* o_full = p_full + kQT;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
+  uint64_t* s_full = q_full + kQT;
+  uint64_t* p_half = s_full + kQT;            // [query tile][half of the weights]
+  uint64_t* o_full = p_half + 2 * kQT;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + kQT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kSoft = 4 * kQT;               // softmax warps
   const int hk = blockIdx.y;
@@ -224,16 +459,17 @@ __global__ void __launch_bounds__(TcGeom<kQT>::kThreads, kQT == 2 ? 1 : 2)
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], kQT);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], kQT);
     }
-    mbar_init(q_full, kSoft);
     for (int t = 0; t < kQT; ++t) {
+      mbar_init(&q_full[t], 4);
+      mbar_init(&o_full[t], 1);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_full[t], 4);
+      mbar_init(&p_half[2 * t], 4);
+      mbar_init(&p_half[2 * t + 1], 4);
     }
-    mbar_init(o_full, 1);
     fence_mbar_init();
   }
   if (warp == kSoft + 1) tmem_alloc(tmem_slot, G::kTmem);
@@ -241,6 +477,43 @@ __global__ void __launch_bounds__(TcGeom<kQT>::kThreads, kQT == 2 ? 1 : 2)
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = *tmem_slot;
+
+  if (warp < kSoft) {
+    // A softmax warp's 32 rows into the swizzled Q tile, a row's 16-byte chunks to
+    // neighbouring lanes, all loads in flight together; a negative scale goes into
+    // their signs.  Before the wait for the decoded tiles: whatever wrote the
+    // queries was complete before the decoding kernel let this one start.
+    constexpr int kNc = d16 / 8, kDr = 32 / kNc, kDc = 32 - kDr * kNc;   // a step of 32 items
+    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+    const int t = warp >> 2;
+    int qr = lane / kNc, qc = lane - qr * kNc;
+    uint8_t* tile = sq + t * img;
+    uint4 x[kNc];
+#pragma unroll
+    for (int k = 0; k < kNc; ++k) {
+      const int rg = r0 + t * kQr + (warp & 3) * 32 + qr;
+      x[k] = make_uint4(0, 0, 0, 0);
+      if (rg < a.rows && 8 * qc < a.D) {
+        const int mm = a.group.div(rg), hh = hk * a.group.d + rg - mm * a.group.d;
+        x[k] = __ldg(reinterpret_cast<const uint4*>(a.q + b * a.qb + mm * a.qm + hh * a.qh) + qc);
+      }
+      qr += kDr;
+      qc += kDc;
+      if (qc >= kNc) qc -= kNc, ++qr;
+    }
+    qr = lane / kNc, qc = lane - qr * kNc;
+#pragma unroll
+    for (int k = 0; k < kNc; ++k) {
+      *reinterpret_cast<uint4*>(tile + panel_chunk(d16, (warp & 3) * 32 + qr, qc)) =
+          make_uint4(x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip);
+      qr += kDr;
+      qc += kDc;
+      if (qc >= kNc) qc -= kNc, ++qr;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&q_full[t]);
+  }
   pdl_wait_then_trigger();
 
   const int len = seq_len(a, b);
@@ -249,10 +522,13 @@ __global__ void __launch_bounds__(TcGeom<kQT>::kThreads, kQT == 2 ? 1 : 2)
   const int end = min(begin + a.chunk, last_limit);
   const int n = end > begin ? (end - begin + kKv - 1) / kKv : 0;
   const int tile0 = begin / kKv;
+  // Words of 32 positions of tile j that any row of the block sees.
+  auto words = [&](int j) { return min(4, (end - begin - j * kKv + 31) >> 5); };
 
-  if (warp == kSoft) {
-    // ------------------------------------------------------------ loads
-    if (lane == 0) {
+  if (warp >= kSoft) {
+    regs_down<G::kRestRegs>();
+    if (warp == kSoft && lane == 0) {
+      // ---------------------------------------------------------- loads
       const uint8_t* src = a.images + ((b * a.view.heads + hk) * a.tiles + tile0) * (2ll * img);
       bool ok = true;
       int j = 0;
@@ -278,155 +554,121 @@ __global__ void __launch_bounds__(TcGeom<kQT>::kThreads, kQT == 2 ? 1 : 2)
         }
       }
     }
-    __syncwarp();
-  } else if (warp == kSoft + 1) {
-    // -------------------------------------------------------------- MMAs
-    if (lane == 0 && n > 0) {
-      const uint32_t id_s = idesc_bf16(kKv), id_o = idesc_bf16(d16);
-      auto scores = [&](int t, int s) {
-        for (int k = 0; k < d16 / 16; ++k)
-          mma_ss(tmem + t * kKv, smem_desc_sw32(smem_addr(sq + t * img + k * (kQr * 32))),
-                 smem_desc_sw32(smem_addr(sk + s * img + k * (kKv * 32))), id_s, k != 0);
-        mma_commit(&s_full[t]);
-      };
-      bool ok = mbar_wait(q_full, 0) && mbar_wait(&k_full[0], 0);
-      tmem_fence_after();
-      if (ok) {
-        for (int t = 0; t < kQT; ++t) scores(t, 0);
-        mma_commit(&k_empty[0]);
-      }
-      for (int j = 0; j < n && ok; ++j) {
-        const int s = j % kStages, sn = (j + 1) % kStages;
-        for (int t = 0; t < kQT && ok; ++t) {
-          ok = mbar_wait(&p_full[t], j & 1);
-          if (ok && t == 0) ok = mbar_wait(&v_full[s], (j / kStages) & 1);
-          if (!ok) break;
-          tmem_fence_after();
-          for (int k = 0; k < kKv / 16; ++k)
-            mma_ts(tmem + kQT * kKv + t * 128, tmem + t * kKv + 8 * k,
-                   smem_desc_sw32(smem_addr(sv + s * img + k * (d16 * 32))), id_o, (j | k) != 0);
-          if (t == kQT - 1) mma_commit(&v_empty[s]);
-          if (j + 1 < n) {
-            // The next scores take the place of these weights: MMAs of one
-            // thread run in the order of their issue.
-            if (t == 0) ok = mbar_wait(&k_full[sn], ((j + 1) / kStages) & 1);
-            if (!ok) break;
-            tmem_fence_after();
-            scores(t, sn);
-            if (t == kQT - 1) mma_commit(&k_empty[sn]);
-          }
+    if (warp > kSoft && warp <= kSoft + kQT && n > 0) {
+      // ------------------------------------- MMAs, a warp per query tile
+      // Warp reductions and votes hand their results over in uniform registers.
+      constexpr uint32_t kAll = 0xFFFFFFFFu;
+      const uint32_t tm = __reduce_max_sync(kAll, tmem);
+      const int n_u = __reduce_max_sync(kAll, n), span = __reduce_max_sync(kAll, end - begin);
+      const int t = __reduce_max_sync(kAll, warp) - kSoft - 1;
+      auto words_u = [&](int j) { return min(4, (span - j * kKv + 31) >> 5); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_spin(bar, parity); };
+      if (elect_one()) {
+      constexpr uint32_t id_o = idesc_bf16(d16);
+      const uint32_t aq = smem_addr(sq) + t * img, ak = smem_addr(sk), av = smem_addr(sv);
+      const uint32_t ts = tm + t * kKv, to = tm + kQT * kKv + t * 128;
+      // S of tile j, in K stage s; with it that stage has been read.
+      auto scores = [&](int s, int j) {
+        const uint32_t kk = ak + s * img;
+        const uint32_t id = idesc_bf16(0) | static_cast<uint32_t>(words_u(j)) << 19;    // N = 32 words
+        {
+#pragma unroll
+          for (int k = 0; k < d16 / 16; ++k)
+            mma_ss(ts, panel_desc<kD16>(aq, k), panel_desc<kD16>(kk, k), id, k != 0);
+          mma_commit(&s_full[t]);
+          mma_commit(&k_empty[s]);
         }
+      };
+      // K steps (16 positions) first .. first + 3 of the second product.
+      auto output = [&](int s, int first, int n_k, bool fresh) {
+        const uint64_t v = smem_desc_sw128(av + s * img) + first * (d16 * 32) / 16;
+        if (n_k >= 4) {
+          {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts(to, ts + 8 * (first + k), v + 2 * k, id_o, k != 0 || !fresh);
+          }
+        } else if (n_k > 0) {
+          for (int k = 0; k < n_k; ++k)
+            mma_ts(to, ts + 8 * (first + k), v + 2 * k, id_o, k != 0 || !fresh);
+        }
+      };
+      bool ok = wait(&q_full[t], 0) && wait(&k_full[0], 0);
+      tmem_fence_after();
+      if (ok) scores(0, 0);
+      for (int j = 0; j < n_u && ok; ++j) {
+        const int s = j % kStages, sn = (j + 1) % kStages;
+        const int steps = 2 * words_u(j);
+        // The loads first: they are there long before the weights.  With one
+        // stage the next K follows the end of these scores' products.
+        ok = wait(&v_full[s], (j / kStages) & 1);
+        if (j + 1 < n_u) ok = ok && wait(&k_full[sn], ((j + 1) / kStages) & 1);
+        ok = ok && wait(&p_half[2 * t], j & 1);
+        if (!ok) break;
+        tmem_fence_after();
+        output(s, 0, min(steps, 4), j == 0);
+        if (!(ok = wait(&p_half[2 * t + 1], j & 1))) break;
+        tmem_fence_after();
+        output(s, 4, steps - 4, false);
+        mma_commit(&v_empty[s]);
+        // The next scores take the place of these weights: MMAs of one thread
+        // run in the order of their issue.
+        if (j + 1 < n_u) scores(sn, j + 1);
       }
       if (!ok) atomicOr(a.err, kErrConsumerWait);
       // Every MMA has completed before the epilogue, and before the columns
       // are released.
-      mma_commit(o_full);
-      mbar_wait(o_full, 0);
+      mma_commit(&o_full[t]);
+      mbar_wait(&o_full[t], 0);
+      }
     }
     __syncwarp();
   } else {
     // ----------------------------------------------------------- softmax
+    regs_up<G::kSoftRegs>();
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
     const int r = r0 + t * kQr + row;
     const bool mine = r < a.rows;
     const int m = mine ? a.group.div(r) : 0, h = hk * a.group.d + (mine ? r - m * a.group.d : 0);
     // Not zero: a masked score, -inf, stays -inf through it.
     const float sc = fmaxf(fabsf(a.scale_log2) * kUnscale, 1e-38f);
-    {
-      // The row into the swizzled Q tile; a negative scale goes into its signs.
-      const uint16_t* src = a.q + b * a.qb + m * a.qm + h * a.qh;
-      const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-      const int sw = (row >> 2) & 1;
-      uint8_t* dst = sq + t * img + row * 32;
-      for (int c = 0; c < d16 / 8; ++c) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (mine && 8 * c < a.D) x = __ldg(reinterpret_cast<const uint4*>(src) + c);
-        x.x ^= flip, x.y ^= flip, x.z ^= flip, x.w ^= flip;
-        *reinterpret_cast<uint4*>(dst + (c >> 1) * (kQr * 32) + 16 * ((c & 1) ^ sw)) = x;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-    }
     const int limit = row_limit(a, len, r);
     const int tile_limit = row_limit(a, len, min(r0 + t * kQr, a.rows - 1));   // the fewest of the tile
     const uint32_t ts = tmem + (uint32_t((warp & 3) * 32) << 16) + t * kKv;
     const uint32_t to = tmem + (uint32_t((warp & 3) * 32) << 16) + kQT * kKv + t * 128;
     float mx = -INFINITY, l = 0.0f;
     bool ok = true;
+    if (t == 1 && n > 0) next_turn<kQT>(warp);             // the first turn is tile 0's
     for (int j = 0; j < n; ++j) {
+      if (!ok) {
+        // Gave up: the other tile's turns go on.
+        my_turn<kQT>(warp);
+        if (t == 0 || j + 1 < n) next_turn<kQT>(warp);
+        continue;
+      }
       const uint4 there = __ldg(a.tile_mask + b * a.tiles + tile0 + j);
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_full[t], j & 1))) {
-        ok = false;
-        break;
+      ok = __all_sync(0xFFFFFFFFu, mbar_spin(&s_full[t], j & 1));
+      if (!ok) {
+        --j;
+        continue;
       }
       tmem_fence_after();
-      uint32_t x[4][32];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) tmem_ld32(ts + 32 * v, x[v]);
-      tmem_wait_ld();
       const int pos0 = begin + j * kKv;
+      uint32_t see[4] = {there.x, there.y, there.z, there.w};
       if (pos0 + kKv > tile_limit || (there.x & there.y & there.z & there.w) != 0xFFFFFFFFu) {
-        const uint32_t w[4] = {there.x, there.y, there.z, there.w};
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int left = limit - pos0 - 32 * v;          // positions of this word the row sees
-          const uint32_t see = left >= 32 ? w[v] : left <= 0 ? 0u : w[v] & ((1u << left) - 1u);
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!(see >> e & 1)) x[v][e] = 0xFF800000u;    // -inf
+          see[v] = left >= 32 ? see[v] : left <= 0 ? 0u : see[v] & ((1u << left) - 1u);
         }
+        softmax_tile<false, kD16, kQT>(ts, to, sc, mx, l, j == 0, see, words(j), p_half + 2 * t, warp, lane,
+                                        t == 1 && j + 1 == n);
+      } else {
+        softmax_tile<true, kD16, kQT>(ts, to, sc, mx, l, j == 0, see, 4, p_half + 2 * t, warp, lane,
+                                        t == 1 && j + 1 == n);
       }
-      float top[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        top[v] = fmaxf(__uint_as_float(x[v][0]), __uint_as_float(x[v][1]));
-#pragma unroll
-        for (int e = 2; e < 32; e += 2)
-          top[v] = max3(top[v], __uint_as_float(x[v][e]), __uint_as_float(x[v][e + 1]));
-      }
-      const float peak = max3(top[0], top[1], fmaxf(top[2], top[3]));
-      const float peak2 = peak * sc;
-      if (__any_sync(0xFFFFFFFFu, peak2 > mx + 8.0f)) {
-        const float m_new = fmaxf(mx, peak2);
-        const float alpha = m_new == -INFINITY ? 1.0f : ex2(mx - m_new);
-        mx = m_new;
-        l *= alpha;
-        // These scores were issued after the last weights' product, so O is
-        // complete.
-        if (j > 0) {
-          for (int c = 0; c < d16 / 16; ++c) {
-            uint32_t o[16];
-            tmem_ld16(to + 16 * c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st16(to + 16 * c, o);
-          }
-        }
-      }
-      const float shift = kShift - (mx == -INFINITY ? 0.0f : mx);
-      float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        uint32_t p[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float p0 = ex2(fmaf(__uint_as_float(x[v][2 * e]), sc, shift));
-          const float p1 = ex2(fmaf(__uint_as_float(x[v][2 * e + 1]), sc, shift));
-          sum[v] += p0 + p1;
-          // Rounded to bf16, the type of the product; the sum is taken before.
-          p[e] = bf16x2(p0, p1);
-        }
-        tmem_st16(ts + 16 * v, p);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tmem_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
     }
-    if (ok && n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_full, 0));
+    if (ok && n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[t], 0));
     if (!ok) {
       if (lane == 0) atomicOr(a.err, kErrConsumerWait);
     } else {
@@ -436,30 +678,39 @@ __global__ void __launch_bounds__(TcGeom<kQT>::kThreads, kQT == 2 ? 1 : 2)
       const float inv = l > 0.0f ? kUnscale / l : 0.0f;
       uint16_t* out = a.out + b * a.ob + m * a.om + h * a.oh;
       float* po = a.part_o + at * (32 * a.view.nb);
-      for (int c = 0; c < d16 / 16; ++c) {
-        uint32_t o[16];
+      // 32 channels at a time.
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = 0;
+      for (int c = 0; c < d16; c += 32) {
+        uint32_t o[2][16];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[u][e] = 0;
         if (n > 0) {
-          tmem_ld16(to + 16 * c, o);
+          tmem_ld16(to + c, o[0]);
+          if (c + 16 < d16) tmem_ld16(to + c + 16, o[1]);
           tmem_wait_ld();
         }
-        if (!mine) continue;
-        if (part) {
-          if (mx != -INFINITY)
+        if (!mine || (part && mx == -INFINITY)) continue;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          if (c + 16 * u >= d16) continue;
+          if (part) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<uint4*>(po + 16 * c + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          continue;
-        }
+              *reinterpret_cast<uint4*>(po + c + 16 * u + e) =
+                  make_uint4(o[u][e], o[u][e + 1], o[u][e + 2], o[u][e + 3]);
+            continue;
+          }
 #pragma unroll
-        for (int e = 0; e < 16; e += 8) {
-          if (16 * c + e >= a.D) continue;
-          uint32_t w[4];
+          for (int e = 0; e < 16; e += 8) {
+            if (c + 16 * u + e >= a.D) continue;
+            uint32_t w[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            w[k] = bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-          *reinterpret_cast<uint4*>(out + 16 * c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int k = 0; k < 4; ++k)
+              w[k] = bf16x2(__uint_as_float(o[u][e + 2 * k]) * inv, __uint_as_float(o[u][e + 2 * k + 1]) * inv);
+            *reinterpret_cast<uint4*>(out + c + 16 * u + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
         }
       }
       if (mine && part) a.part_ml[at] = make_float2(mx, l);
@@ -476,17 +727,35 @@ __global__ void __launch_bounds__(TcGeom<kQT>::kThreads, kQT == 2 ? 1 : 2)
   }
 }
 
-template <int kQT>
+// setmaxnreg draws on what the block was launched with: were that less than the
+// warpgroups' shares, the kernel would wait for good.
+template <int kQT, int kD16>
+bool registers_suffice() {
+  using G = TcGeom<kQT, kD16>;
+  static const int regs = [] {
+    cudaFuncAttributes f{};
+    return cudaFuncGetAttributes(&f, attn_tc_kernel<kQT, kD16>) == cudaSuccess ? f.numRegs : 0;
+  }();
+  return regs * (kQT + 1) >= kQT * G::kSoftRegs + G::kRestRegs;
+}
+
+template <int kQT, int kD16>
 int launch_tc(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
-  using G = TcGeom<kQT>;
-  const int rc = allow_smem<attn_tc_kernel<kQT>>(G::smem(128), dev);
+  using G = TcGeom<kQT, kD16>;
+  const int rc = allow_smem<attn_tc_kernel<kQT, kD16>>(G::kSmem, dev);
   if (rc != KQ_OK) return rc;
+  if (!registers_suffice<kQT, kD16>()) return record_cuda_error(cudaErrorLaunchOutOfResources);
   const int64_t row_tiles = (a.rows + kQT * kQr - 1) / (kQT * kQr);
   if (row_tiles * p.n_chunks >= (int64_t(1) << 31)) return KQ_ERR_INVALID;
   const dim3 grid(static_cast<unsigned>(row_tiles * p.n_chunks), static_cast<unsigned>(a.view.heads),
                   static_cast<unsigned>(batch));
-  const cudaError_t e = launch_pdl(attn_tc_kernel<kQT>, grid, dim3(G::kThreads), G::smem(a.d16), st, a);
+  const cudaError_t e = launch_pdl(attn_tc_kernel<kQT, kD16>, grid, dim3(G::kThreads), G::kSmem, st, a);
   return e == cudaSuccess ? KQ_OK : record_cuda_error(e);
+}
+
+template <int kD16>
+int launch_tc_qt(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
+  return p.q_tiles == 2 ? launch_tc<2, kD16>(a, p, batch, dev, st) : launch_tc<1, kD16>(a, p, batch, dev, st);
 }
 
 }  // namespace
@@ -498,7 +767,16 @@ int launch_attention_tc(const AttnArgs& a, const AttnPlan& p, int64_t batch, int
       dim3(static_cast<unsigned>(p.tiles), static_cast<unsigned>(2 * a.view.heads), static_cast<unsigned>(batch)),
       dim3(kDecodeThreads), 0, st, a, const_cast<uint4*>(a.tile_mask), const_cast<uint8_t*>(a.images));
   if (e != cudaSuccess) return record_cuda_error(e);
-  return p.q_tiles == 2 ? launch_tc<2>(a, p, batch, dev, st) : launch_tc<1>(a, p, batch, dev, st);
+  switch (a.d16) {
+    case 16: return launch_tc_qt<16>(a, p, batch, dev, st);
+    case 32: return launch_tc_qt<32>(a, p, batch, dev, st);
+    case 48: return launch_tc_qt<48>(a, p, batch, dev, st);
+    case 64: return launch_tc_qt<64>(a, p, batch, dev, st);
+    case 80: return launch_tc_qt<80>(a, p, batch, dev, st);
+    case 96: return launch_tc_qt<96>(a, p, batch, dev, st);
+    case 112: return launch_tc_qt<112>(a, p, batch, dev, st);
+    default: return launch_tc_qt<128>(a, p, batch, dev, st);
+  }
 }
 
 }  // namespace kq

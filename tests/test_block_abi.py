@@ -107,22 +107,13 @@ def test_binding_refuses_host_tensors(L):
         L.KVCache(t, t[..., :2].contiguous(), t, t[..., :2].contiguous(), 64)
     with pytest.raises(ValueError):
         L.KVCache(t, t, t, t, 60)
-    q = torch.zeros((1, 1, 2, 64), dtype=torch.bfloat16)
-    with pytest.raises(ValueError):
-        L._head_rows(q, torch.bfloat16, "q", q.device)
-
-
-def test_overlapping_output_rows_are_refused(L):
-    x = torch.zeros(4096)
-    for shape, strides, ok in (((2, 3, 4, 8), (96, 32, 8, 1), True), ((2, 3, 4, 8), (96, 8, 24, 1), True),
-                               ((2, 3, 4, 8), (0, 32, 8, 1), False), ((2, 3, 4, 8), (96, 32, 4, 1), False),
-                               ((1, 3, 4, 8), (0, 40, 8, 1), True), ((2, 3, 4, 8), (95, 32, 8, 1), False)):
-        t = x.as_strided(shape, strides)
-        if ok:
-            L._disjoint_rows(t, "out")
-        else:
-            with pytest.raises(ValueError):
-                L._disjoint_rows(t, "out")
+    u8 = torch.zeros((16, 32), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="qa must be a CUDA tensor"):
+        L.gemm_mxfp4_epilogue(u8, u8, u8, u8)
+    with pytest.raises(ValueError, match="qa must be a CUDA tensor"):
+        L.gemm_mxfp4_epilogue(None, u8, u8, u8)
+    with pytest.raises(ValueError, match="activation"):
+        L.gemm_mxfp4_epilogue(u8, u8, u8, u8, activation="relu")
 
 
 def epilogue(L, qa=FAKE, sa=FAKE, qb=FAKE, sb=FAKE, M=4, N=8, K=64, bias=None, act=0, gate=None, tokens=0,

@@ -219,3 +219,31 @@ def test_graph_replay_and_another_stream():
     page = o.unpack_codes(cache.k_codes[1, :, 1].cpu().numpy())
     assert np.array_equal(page, o.unpack_codes(q[0, 0]))
     del g
+
+
+def test_refusals():
+    cache = pool(4, 16, 2, 64)
+    table = i32([[0, 1], [2, 3]])
+    k = draw((2, 20, 2, 64), 15).to(DEV)
+    lens = i32([20, 20])
+    odd = torch.zeros((2, 20, 2, 68), dtype=torch.bfloat16, device=DEV)[..., 4:]
+    for bad in (lambda: kq.cache_write(cache, table, k.float(), k), lambda: kq.cache_write(cache, table, k, k[:, :19]),
+                lambda: kq.cache_write(cache, table, k[:, :, :1], k[:, :, :1]),
+                lambda: kq.cache_write(cache, table[:1], k, k), lambda: kq.cache_write(cache, table.long(), k, k),
+                lambda: kq.cache_write(cache, table, k, k, lens=lens[:1]),
+                lambda: kq.cache_write(cache, table, k, k, start=lens.long()),
+                lambda: kq.cache_write(cache, table, odd, k), lambda: kq.cache_write(cache, table, k, k.cpu()),
+                lambda: kq.cache_write(cache, table, k.transpose(2, 3), k),
+                lambda: kq.cache_write(cache, table.t(), k, k),
+                lambda: kq.cache_read(cache, table, lens, -1), lambda: kq.cache_read(cache, table, lens[:1], 4),
+                lambda: kq.cache_read(cache, table, lens, 20, out_dtype=torch.float16),
+                lambda: kq.cache_read(cache, table, lens, 20, k=k[:, :19]),
+                lambda: kq.cache_read(cache, table, lens, 20, k=k.float()),
+                lambda: kq.cache_read(cache, table, lens, 20, k=k[:, :1].expand(-1, 20, -1, -1)),
+                lambda: kq.cache_read(cache, table, lens, "20"),
+                lambda: kq.KVCache(cache.k_codes, cache.k_scales, cache.v_codes[:2], cache.v_scales, 64),
+                lambda: kq.KVCache(cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, 96),
+                lambda: kq.cache_alloc(4, 24, 2, 64, device=DEV)):
+        with pytest.raises(ValueError):
+            bad()
+    assert kq.device_status() == 0

@@ -4,11 +4,15 @@ Argument marshalling only: tensors are checked for device, dtype, shape and
 contiguity, their device pointers and the current CUDA stream are passed to
 the library, and a non-zero status raises.  Every step of the computation runs
 in the library's kernels; there is no CPU fallback, and a missing library
-raises ImportError.
+raises ImportError.  The calls of the block operators (product with epilogue,
+K/V cache, attention) do this in ``_kq_torch.so`` (``csrc/kq_torch.cpp``), over the
+same entry points.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -122,6 +126,28 @@ def lib():
 def _check(name: str, status: int) -> None:
     if status != KQ_OK:
         raise KQError(name, status, lib())
+
+
+BINDING_PATH = os.path.join(_HERE, "_kq_torch.so")
+_BINDING = None
+
+
+def _binding():
+    """The compiled part of the binding, over the loaded library's entry points."""
+    global _BINDING
+    if _BINDING is None:
+        if not os.path.exists(BINDING_PATH):
+            raise ImportError(f"{BINDING_PATH} is missing: build it first "
+                              "(python -c 'import __graft_entry__ as g; g.build()')")
+        loader = importlib.machinery.ExtensionFileLoader("_kq_torch", BINDING_PATH)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("_kq_torch", BINDING_PATH, loader=loader))
+        loader.exec_module(module)
+        module.bind(_check, *(ctypes.cast(getattr(lib(), n), ctypes.c_void_p).value for n in (
+            "kq_gemm_mxfp4_epilogue", "kq_scales_tiled_bytes", "kq_cache_write", "kq_cache_read",
+            "kq_attention_mxfp4", "kq_attention_workspace_bytes")))
+        _BINDING = module
+    return _BINDING
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -602,49 +628,13 @@ def gemm_mxfp4_epilogue(qa: torch.Tensor, sa_tiled: torch.Tensor, qb: torch.Tens
     layer's product.  bias bf16 [N]; activation "none", "gelu_tanh", "gelu" or
     "silu"; gate bf16 [samples, N] with samples >= ceil(M / tokens_per_sample);
     residual [M, N] of out's type, and ``out=residual`` adds in place."""
-    for t, n in ((qa, "qa"), (sa_tiled, "sa_tiled"), (qb, "qb"), (sb_tiled, "sb_tiled")):
-        _dev_tensor(t, torch.uint8, n)
-    if qa.dim() != 2 or qb.dim() != 2 or qa.shape[1] == 0 or qa.shape[1] % 16 != 0:
-        raise ValueError("qa must be [M, K/2] and qb [N, K/2], K a multiple of 32")
-    M, K = qa.shape[0], 2 * qa.shape[1]
-    N = qb.shape[0]
-    if qb.shape[1] != K // 2:
-        raise ValueError("qb must be [N, K/2]")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
-    if out_dtype not in (torch.float32, torch.bfloat16):
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be float32 or bfloat16")
-    size = lib().kq_scales_tiled_bytes
-    if sa_tiled.numel() < size(M, K) or sb_tiled.numel() < size(N, K):
-        raise ValueError("tiled scale arrays are too small")
-    if bias is not None:
-        _dev_tensor(bias, torch.bfloat16, "bias")
-        if tuple(bias.shape) != (N,):
-            raise ValueError("bias must be bf16 [N]")
-    if gate is not None:
-        _dev_tensor(gate, torch.bfloat16, "gate")
-        if tokens_per_sample is None or int(tokens_per_sample) < 1:
-            raise ValueError("a gate needs tokens_per_sample >= 1")
-        if gate.dim() != 2 or gate.shape[1] != N or gate.shape[0] < -(-M // int(tokens_per_sample)):
-            raise ValueError("gate must be bf16 [B, N] with B >= ceil(M / tokens_per_sample)")
-    if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=qa.device)
-    for t, n in ((out, "out"), (residual, "residual")):
-        if t is not None:
-            _dev_tensor(t, out_dtype, n)
-            if tuple(t.shape) != (M, N):
-                raise ValueError(f"{n} must be [M, N]")
-    if residual is not None and M * N and residual.data_ptr() != out.data_ptr() and \
-            abs(residual.data_ptr() - out.data_ptr()) < M * N * out.element_size():
-        raise ValueError("residual must be out itself or not overlap it")
-    for t in (sa_tiled, qb, sb_tiled, bias, gate, residual, out):
-        if t is not None and t.device != qa.device:
-            raise ValueError("the operands must be on one device")
-    _call("kq_gemm_mxfp4_epilogue", qa.device, qa.data_ptr(), sa_tiled.data_ptr(), qb.data_ptr(),
-          sb_tiled.data_ptr(), M, N, K, _ptr(bias), ACTIVATIONS[activation], _ptr(gate),
-          0 if gate is None else int(tokens_per_sample), _ptr(residual), out.data_ptr(),
-          KQ_OUT_F32 if out_dtype == torch.float32 else KQ_OUT_BF16)
-    return out
+    return (_BINDING or _binding()).epilogue(
+        qa, sa_tiled, qb, sb_tiled, bias, ACTIVATIONS[activation], gate, tokens_per_sample, residual,
+        out, out_dtype is torch.float32)
 
 
 class _CacheStruct(ctypes.Structure):
@@ -659,7 +649,7 @@ class KVCache:
     makes new ones."""
 
     __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "pages", "page_size", "heads",
-                 "head_dim", "device", "_c", "_ptr")
+                 "head_dim", "device", "_c", "_ptr", "_index")
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
                  v_scales: torch.Tensor, head_dim: int):
@@ -688,6 +678,7 @@ class KVCache:
         self._c = _CacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                                v_scales.data_ptr(), pages, page_size, heads, head_dim)
         self._ptr = ctypes.addressof(self._c)
+        self._index = self.device.index
 
 
 def cache_alloc(pages: int, page_size: int, heads: int, head_dim: int, device="cuda") -> KVCache:
@@ -699,85 +690,13 @@ def cache_alloc(pages: int, page_size: int, heads: int, head_dim: int, device="c
     return KVCache(make(16 * nb), make(nb), make(16 * nb), make(nb), head_dim)
 
 
-def _call(name: str, device: torch.device, *args):
-    """Calls an entry point on the current stream of ``device``, with that
-    device current."""
-    fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, _stream(device))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream(device))
-    _check(name, st)
-
-
-def _cache_index(cache: KVCache, block_table: torch.Tensor, batch: int, per_seq):
-    """Checks a block table and int32 [batch] arrays on the cache's device."""
-    _dev_tensor(block_table, torch.int32, "block_table")
-    if block_table.dim() != 2 or block_table.shape[0] != batch or block_table.shape[1] < 1:
-        raise ValueError("block_table must be int32 [batch, pages of a sequence]")
-    if block_table.device != cache.device:
-        raise ValueError("block_table must be on the cache's device")
-    for t, n in per_seq:
-        if t is not None:
-            _dev_tensor(t, torch.int32, n)
-            if tuple(t.shape) != (batch,) or t.device != cache.device:
-                raise ValueError(f"{n} must be int32 [batch] on the cache's device")
-
-
-def _head_rows(x: torch.Tensor, dtype, name: str, device):
-    """Checks [batch, rows, heads, head_dim] rows of unit channel stride whose
-    rows start on 16-byte boundaries; returns the strides of the first three
-    (0 for a dimension of size 1, whose stride has no meaning)."""
-    if not isinstance(x, torch.Tensor) or x.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if x.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.device != device:
-        raise ValueError(f"{name} must be on the cache's device")
-    if x.dim() != 4:
-        raise ValueError(f"{name} must be [batch, rows, heads, head_dim]")
-    strides = x.stride()
-    if strides[3] != 1 and x.shape[3] > 1:
-        raise ValueError(f"{name} must have unit stride along head_dim")
-    unit = 16 // x.element_size()
-    sb, st, sh = (s if n > 1 else 0 for s, n in zip(strides, x.shape[:3]))
-    if sb % unit or st % unit or sh % unit or x.data_ptr() % 16:
-        raise ValueError(f"every row of {name} must start on a 16-byte boundary")
-    return sb, st, sh
-
-
-def _disjoint_rows(x: torch.Tensor, name: str):
-    """An output's rows must not overlap one another."""
-    if x.is_contiguous():
-        return
-    reach = 0
-    for s, n in sorted((s, n) for s, n in zip(x.stride(), x.shape) if n > 1):
-        if s <= reach:
-            raise ValueError(f"the rows of {name} overlap")
-        reach += s * (n - 1)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def cache_write(cache: KVCache, block_table: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                 start=None, lens=None) -> KVCache:
     """Quantizes rows into the cache: row t < lens[b] (default: every row) of
     bf16 k and v [batch, tokens, heads, head_dim] goes to position start[b] + t
     (default: t) of sequence b, page block_table[b, position // page_size].
     Everything else in the cache stays as it was."""
-    ks = _head_rows(k, torch.bfloat16, "k", cache.device)
-    vs = _head_rows(v, torch.bfloat16, "v", cache.device)
-    if v.shape != k.shape:
-        raise ValueError("k and v must have the same shape")
-    B, T, H, D = k.shape
-    if H != cache.heads or D != cache.head_dim:
-        raise ValueError("k and v must have the cache's heads and head_dim")
-    _cache_index(cache, block_table, B, ((start, "start"), (lens, "lens")))
-    _call("kq_cache_write", cache.device, cache._ptr, block_table.data_ptr(), B,
-          block_table.shape[1], k.data_ptr(), *ks, v.data_ptr(), *vs, T, _ptr(start), _ptr(lens))
+    (_BINDING or _binding()).cache_write(cache._ptr, cache._index, block_table, k, v, start, lens)
     return cache
 
 
@@ -786,26 +705,10 @@ def cache_read(cache: KVCache, block_table: torch.Tensor, lens, tokens: int, sta
     """Rows of the cache decoded: (k, v), [batch, tokens, heads, head_dim] bf16
     or float32; row t < lens[b] (lens None: every row) is position start[b] + t,
     the others are zeros."""
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be int32 [batch, pages of a sequence]")
-    shape = (block_table.shape[0], int(tokens), cache.heads, cache.head_dim)
-    _cache_index(cache, block_table, shape[0], ((start, "start"), (lens, "lens")))
-    if k is None:
-        k = torch.empty(shape, dtype=out_dtype, device=cache.device)
-    if v is None:
-        v = torch.empty(shape, dtype=out_dtype, device=cache.device)
-    ks = _head_rows(k, out_dtype, "k", cache.device)
-    vs = _head_rows(v, out_dtype, "v", cache.device)
-    if tuple(k.shape) != shape or tuple(v.shape) != shape:
-        raise ValueError("k and v must be [batch, tokens, heads, head_dim]")
-    _disjoint_rows(k, "k")
-    _disjoint_rows(v, "v")
-    _call("kq_cache_read", cache.device, cache._ptr, block_table.data_ptr(), shape[0],
-          block_table.shape[1], shape[1], _ptr(start), _ptr(lens), k.data_ptr(), *ks, v.data_ptr(),
-          *vs, KQ_OUT_F32 if out_dtype == torch.float32 else KQ_OUT_BF16)
-    return k, v
+    return (_BINDING or _binding()).cache_read(cache._ptr, cache._index, block_table, lens, tokens,
+                                               start, out_dtype is torch.float32, k, v)
 
 
 def attention_workspace_bytes(batch: int, M: int, heads: int, kv_heads: int, head_dim: int,
@@ -824,42 +727,10 @@ def attention_mxfp4(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     defaults to head_dim^-0.5, max_len (a bound on lens) to what the block table
     holds.  lse: an optional float32 [batch, heads, M] output.  A row that sees
     no position gives 0, and -inf in lse.  Returns bf16 like q."""
-    qs = _head_rows(q, torch.bfloat16, "q", cache.device)
-    B, M, H, D = q.shape
-    if D != cache.head_dim or H == 0 or H % cache.heads != 0:
-        raise ValueError("q must have the cache's head_dim and a multiple of its heads")
     if lens is None:
         raise ValueError("lens must be int32 [batch]")
-    _cache_index(cache, block_table, B, ((lens, "lens"),))
-    room = block_table.shape[1] * cache.page_size
-    max_len = room if max_len is None else int(max_len)
-    if max_len < 1 or max_len > room:
-        raise ValueError("max_len must be from 1 to what the block table holds")
-    if out is None:
-        out = torch.empty((B, M, H, D), dtype=torch.bfloat16, device=q.device)
-    os_ = _head_rows(out, torch.bfloat16, "out", cache.device)
-    if out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    _disjoint_rows(out, "out")
-    if lse is not None:
-        _dev_tensor(lse, torch.float32, "lse")
-        if tuple(lse.shape) != (B, H, M) or lse.device != cache.device:
-            raise ValueError("lse must be float32 [batch, heads, M] on the cache's device")
-    if B == 0 or M == 0:
-        return out
-    need = attention_workspace_bytes(B, M, H, cache.heads, D, max_len)
-    if workspace is None:
-        if need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-    else:
-        _dev_tensor(workspace, torch.uint8, "workspace")
-        if workspace.device != cache.device:
-            raise ValueError("workspace must be on the cache's device")
-    _call("kq_attention_mxfp4", cache.device, q.data_ptr(), *qs, B, M, H, cache._ptr,
-          block_table.data_ptr(), block_table.shape[1], lens.data_ptr(), max_len,
-          float(D ** -0.5 if scale is None else scale), int(bool(causal)), out.data_ptr(), *os_,
-          _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel())
-    return out
+    return (_BINDING or _binding()).attention(q, cache._ptr, cache._index, block_table, lens, causal,
+                                              scale, max_len, out, lse, workspace)
 
 
 def inverse_transform(y: torch.Tensor, params: torch.Tensor, x=None):

@@ -173,13 +173,6 @@ __global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(const AttnA
 }
 
 // --------------------------------------------------------------- attention
-// The whole warp runs the loop that issues the MMAs, in uniform control flow,
-// and an elected lane issues each batch of them.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                        uint32_t acc) {
   asm volatile(

@@ -202,13 +202,13 @@ __global__ void __launch_bounds__(kEpThreads, 1)
   pdl_wait_then_trigger();
 
   if (warp == 0) {
-    if (lane == 0 && !pair_produce<kN, kStages>(base, full, empty, &amap, &bmap, &sfamap, &sfbmap,
+    if (elect_one() && !pair_produce<kN, kStages>(base, full, empty, &amap, &bmap, &sfamap, &sfbmap,
                                                 a.tiles, rank, pair, n_pairs))
       atomicOr(a.err, kErrProducerWait);
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0 &&
-        !pair_mma<kN, kStages>(base, full, empty, acc_full, acc_empty, tmem_base, a.tiles, pair,
-                               n_pairs))
+    const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem_base);       // uniform
+    if (rank == 0 && elect_one() &&
+        !pair_mma<kN, kStages>(base, full, empty, acc_full, acc_empty, tm, a.tiles, pair, n_pairs))
       atomicOr(a.err, kErrConsumerWait);
   } else {
     constexpr int kGroups = E::kCols / 32;           // 32-column groups of a thread

@@ -32,6 +32,18 @@ __device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
          (uint64_t(128 >> 4) << 32) | (uint64_t(1) << 46);
 }
 
+// True in one lane of a converged warp.  A role that one thread plays (issuing
+// MMAs and copies) is put in a branch on this, with what its operands are formed
+// from in uniform registers (kernel arguments, block indices, warp reductions):
+// the compiler knows that one lane runs there and forms descriptors in uniform
+// registers, where the instructions take them.  In a branch on `lane == 0` each
+// operand is moved there first, 60 to 100 cycles an MMA.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_addr(bar))

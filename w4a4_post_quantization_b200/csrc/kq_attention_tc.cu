@@ -225,15 +225,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(kQr >> 4) << 24);
 }
 
-template <int kRegs>
-__device__ __forceinline__ void regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
 template <int kQT, int kD16>
 struct TcGeom {
   // Two blocks of one query tile share an SM: 113 KB each.
@@ -249,25 +240,6 @@ struct TcGeom {
   static constexpr int kSmem = 1024 + (kQT + 2 * kStages) * 256 * kD16 + 256;
   static_assert(kSmem <= (kQT == 2 ? 232448 : 115712), "shared memory");
 };
-
-// 2^y for both halves without the special-function unit, for y >= -126: 2^f of
-// the fraction by the polynomial of degree 4 with the least relative error over
-// [-1/2, 1/2] (2.6e-6, by Remez' exchange), the integer into the exponent.
-__device__ __forceinline__ void ex2_poly(f2 y, float& p0, float& p1) {
-  const f2 magic = pack2(12582912.0f, 12582912.0f);         // 1.5 2^23: rounds to an integer
-  const f2 r = add2(y, magic);
-  const f2 f = sub2(y, sub2(r, magic));
-  f2 q = fma2(f, pack2(0.009570102207362652f, 0.009570102207362652f),
-              pack2(0.05591785907745361f, 0.05591785907745361f));
-  q = fma2(q, f, pack2(0.240247443318367f, 0.240247443318367f));
-  q = fma2(q, f, pack2(0.6931217908859253f, 0.6931217908859253f));
-  q = fma2(q, f, pack2(0.9999992847442627f, 0.9999992847442627f));
-  float r0, r1, q0, q1;
-  unpack2(r, r0, r1);
-  unpack2(q, q0, q1);
-  p0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(r0) << 23));
-  p1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(r1) << 23));
-}
 
 // mbar_wait as one tight loop, for the waits on every tile's critical path; each
 // poll suspends the warp for a time that the hardware bounds.
@@ -727,10 +699,7 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
 template <int kQT, int kD16>
 bool registers_suffice() {
   using G = TcGeom<kQT, kD16>;
-  static const int regs = [] {
-    cudaFuncAttributes f{};
-    return cudaFuncGetAttributes(&f, attn_tc_kernel<kQT, kD16>) == cudaSuccess ? f.numRegs : 0;
-  }();
+  static const int regs = launched_regs(attn_tc_kernel<kQT, kD16>);
   return regs * (kQT + 1) >= kQT * G::kSoftRegs + G::kRestRegs;
 }
 

@@ -146,6 +146,25 @@ __device__ __forceinline__ f2 sub2(f2 a, f2 b) {
   return d;
 }
 
+// 2^y for both halves without the special-function unit, for y >= -126: 2^f of
+// the fraction by the polynomial of degree 4 with the least relative error over
+// [-1/2, 1/2] (2.6e-6, by Remez' exchange), the integer into the exponent.
+__device__ __forceinline__ void ex2_poly(f2 y, float& p0, float& p1) {
+  const f2 magic = pack2(12582912.0f, 12582912.0f);         // 1.5 2^23: rounds to an integer
+  const f2 r = add2(y, magic);
+  const f2 f = sub2(y, sub2(r, magic));
+  f2 q = fma2(f, pack2(0.009570102207362652f, 0.009570102207362652f),
+              pack2(0.05591785907745361f, 0.05591785907745361f));
+  q = fma2(q, f, pack2(0.240247443318367f, 0.240247443318367f));
+  q = fma2(q, f, pack2(0.6931217908859253f, 0.6931217908859253f));
+  q = fma2(q, f, pack2(0.9999992847442627f, 0.9999992847442627f));
+  float r0, r1, q0, q1;
+  unpack2(r, r0, r1);
+  unpack2(q, q0, q1);
+  p0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(r0) << 23));
+  p1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(r1) << 23));
+}
+
 // Two bf16 values (element 2m in the low half-word) widened exactly to f32.
 __device__ __forceinline__ f2 bf16x2_to_f2(uint32_t w) {
   return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));

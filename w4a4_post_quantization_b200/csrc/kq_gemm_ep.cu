@@ -7,15 +7,16 @@
 // the float32 accumulator on its way out of tensor memory, with one rounding
 // at the end.
 //
-// CTA pairs (kq_gemm.cuh) walk 256 x kN tiles.  Warp 0 loads, warp 1 of the even
-// CTA issues the MMAs, warps 2..9 are the epilogue: two warps for each quarter
-// of the 128 accumulator rows, each taking half of the columns.  A thread holds
-// one row's kN / 2 columns in registers, so the accumulator is handed back as
-// soon as it has been read and the next tile's MMAs run under the activation.
-// The output, and the residual before it, pass through 4 KB boxes of 32 rows x
-// 128 bytes in shared memory, private to a warp: the residual's loads are under
-// way while the tile is still being multiplied, and nothing waits for a store
-// within a tile of bf16.
+// CTA pairs (kq_gemm.cuh) walk 256 x kN tiles.  kN / 16 warps are the epilogue:
+// kN / 64 for each quarter of the 128 accumulator rows, a thread holding 64
+// columns of one row in registers, so the accumulator is handed back as soon as it
+// has been read and the next tile's MMAs run under the activation.  (With 128
+// columns a thread, and half the warps, the activation's chain of dependent
+// instructions was what the kernel waited for: GELU took 8000 cycles a tile.)  One
+// further warp loads, and one of the even CTA issues the MMAs.  The output, and
+// the residual before it, pass through 4 KB boxes of 32 rows x 128 bytes in shared
+// memory, private to a warp: the residual's loads are under way while the tile
+// is still being multiplied.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -31,20 +32,25 @@
 namespace kq {
 namespace {
 
-constexpr int kEpWarps = 8;
-constexpr int kEpThreads = 32 * (2 + kEpWarps);
+constexpr int kCols = 64;                     // columns per epilogue thread
 constexpr int kBoxRows = 32;
 constexpr int kBoxBytes = kBoxRows * 128;
-constexpr int kSlots = 2;                     // boxes per warp
-constexpr int kEpStaging = kEpWarps * kSlots * kBoxBytes;
+constexpr int kEpStaging = 65536;             // the epilogue warps' boxes
 
 template <int kN>
 struct EpGeom {
   static constexpr int kStages = kN == 256 ? 4 : 6;
   using P = PairGeom<kN, kStages>;
-  static constexpr int kCols = kN / 2;        // columns per thread
-  static constexpr int kSmem = 1024 + kStages * P::kStage + kEpStaging +
-                               (2 * kStages + 2 * P::kAcc + kEpWarps) * 8 + 16;
+  static constexpr int kWarps = kN / 16;      // epilogue warps
+  static constexpr int kThreads = 32 * (kWarps + 4);
+  static constexpr int kSlots = kEpStaging / kBoxBytes / kWarps;   // boxes per warp
+  // Registers a thread: wide tiles have 20 warps, launched with 96, of which the
+  // epilogue's take 104 and the others keep 64.
+  static constexpr bool kSplit = kN == 256;
+  static constexpr int kEpRegs = 104, kRestRegs = 64;
+  static constexpr int kVectors = kWarps * 2 * kCols * 4;   // bias and gate of each warp's columns
+  static constexpr int kSmem = 1024 + kStages * P::kStage + kEpStaging + kVectors +
+                               (2 * kStages + 2 * P::kAcc + kWarps) * 8 + 16;
   static_assert(kSmem <= 232448, "shared memory");
 };
 
@@ -66,47 +72,62 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
-// x0 / (1 + 2^t0), x1 / (1 + 2^t1) with one reciprocal: 1 / a = b (1 / ab).
-// t is capped at 60, so the product stays finite; past it the quotients are
-// 2^-60 of x and less (the special-function pipe, not the FMAs, bounds the
-// activations, and this takes a quarter of its work away).
-__device__ __forceinline__ void over_one_plus_exp2(float& x0, float& x1, float t0, float t1) {
-  const float a = 1.0f + ex2_approx(fminf(t0, 60.0f));
-  const float b = 1.0f + ex2_approx(fminf(t1, 60.0f));
+// x / (1 + 2^t) for both halves with one reciprocal: 1 / a = b (1 / ab).  t is
+// capped at 60, so the product stays finite; past it the quotients are 2^-60 of x
+// and less (the special-function unit bounds the activations, and this takes a
+// quarter of its work away; the polynomial exponential of the attention, for every
+// second pair, cost more issue slots than it freed: 38 against 34 us for 8192 x
+// 4608 x 1152 with GELU).
+__device__ __forceinline__ f2 over_one_plus_exp2(f2 x, f2 t) {
+  float t0, t1, a, b;
+  unpack2(t, t0, t1);
+  t0 = fminf(t0, 60.0f);
+  t1 = fminf(t1, 60.0f);
+  a = ex2_approx(t0);
+  b = ex2_approx(t1);
+  unpack2(add2(pack2(a, b), pack2(1.0f, 1.0f)), a, b);
   const float r = rcp_approx(a * b);
-  x0 *= r * b;
-  x1 *= r * a;
+  return mul2(x, mul2(pack2(r, r), pack2(b, a)));
 }
 
 // Two values through the activation.
 template <int kAct>
-__device__ __forceinline__ void activate(float& x0, float& x1) {
+__device__ __forceinline__ f2 activate(f2 x) {
   if constexpr (kAct == KQ_ACT_GELU_TANH) {
     // 0.5 x (1 + tanh u) = x / (1 + exp(-2 u)), u = sqrt(2 / pi) (x + 0.044715 x^3):
     // no difference of near-equal numbers for negative x.
     constexpr float k1 = -2.302208198f;       // -2 sqrt(2 / pi) log2(e)
     constexpr float k3 = -0.1029432408f;      // 0.044715 k1
-    over_one_plus_exp2(x0, x1, x0 * fmaf(k3, x0 * x0, k1), x1 * fmaf(k3, x1 * x1, k1));
+    return over_one_plus_exp2(x, mul2(x, fma2(pack2(k3, k3), mul2(x, x), pack2(k1, k1))));
   } else if constexpr (kAct == KQ_ACT_SILU) {
     constexpr float k = -1.4426950409f;       // -log2(e)
-    over_one_plus_exp2(x0, x1, k * x0, k * x1);
+    return over_one_plus_exp2(x, mul2(x, pack2(k, k)));
   } else if constexpr (kAct == KQ_ACT_GELU) {
     // x Phi(x) with Abramowitz and Stegun 7.1.26:
     //   erfc(z) = t (a1 + t (a2 + ... + a5 t^3)) exp(-z^2) + e, t = 1 / (1 + p z),
-    //   |e| <= 1.5e-7 for z >= 0.
-    float* x[2] = {&x0, &x1};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float v = *x[i], z = fabsf(v) * 0.7071067812f;
-      const float t = rcp_approx(fmaf(0.3275911f, z, 1.0f));
-      float s = fmaf(1.061405429f, t, -1.453152027f);
-      s = fmaf(s, t, 1.421413741f);
-      s = fmaf(s, t, -0.284496736f);
-      s = fmaf(s, t, 0.254829592f);
-      const float q = 0.5f * s * t * ex2_approx(z * z * -1.4426950409f);   // Phi(-|v|)
-      *x[i] = v * (v < 0.0f ? q : 1.0f - q);
-    }
+    //   |e| <= 1.5e-7 for z >= 0; the two reciprocals as above.
+    auto both = [](float k) { return pack2(k, k); };
+    float v0, v1, a, b, z0, z1;
+    unpack2(x, v0, v1);
+    const f2 z = mul2(pack2(fabsf(v0), fabsf(v1)), both(0.7071067812f));
+    unpack2(fma2(z, both(0.3275911f), both(1.0f)), a, b);
+    // 1 + p z is capped so that the product of the two stays finite; Phi is 0 there.
+    a = fminf(a, 1e18f);
+    b = fminf(b, 1e18f);
+    const float r = rcp_approx(a * b);
+    const f2 t = mul2(both(r), pack2(b, a));
+    f2 s = fma2(t, both(1.061405429f), both(-1.453152027f));
+    s = fma2(s, t, both(1.421413741f));
+    s = fma2(s, t, both(-0.284496736f));
+    s = fma2(s, t, both(0.254829592f));
+    unpack2(mul2(mul2(z, z), both(-1.4426950409f)), z0, z1);
+    // Phi(-|v|)
+    const f2 q = mul2(mul2(s, t), mul2(both(0.5f), pack2(ex2_approx(z0), ex2_approx(z1))));
+    float q0, q1;
+    unpack2(q, q0, q1);
+    return mul2(x, pack2(v0 < 0.0f ? q0 : 1.0f - q0, v1 < 0.0f ? q1 : 1.0f - q1));
   }
+  return x;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -115,42 +136,40 @@ __device__ __forceinline__ float bf16_at(const uint16_t* p) {
   return __uint_as_float(static_cast<uint32_t>(__ldg(p)) << 16);
 }
 
-// 32 columns of a row, from column `col`: bias, activation, gate.  kVec: N is
-// a multiple of 8, so a group of 8 columns is inside or outside as one and
-// starts on 16 bytes.
-template <int kAct, bool kVec>
-__device__ __forceinline__ void finish(uint32_t (&x)[32], const EpArgs& a, int col,
-                                       const uint16_t* gate) {
+// 32 columns of a row: bias, activation, gate.  The two vectors come as float32
+// from shared memory (`bias`, `gate`: these columns of the warp's copy), the same
+// address in every lane; a row whose sample differs within the warp has its gate
+// in `own_gate` (column `col` of it; columns from N on are not read).
+template <int kAct>
+__device__ __forceinline__ void finish(uint32_t (&x)[32], const float* bias, const float* gate,
+                                       const uint16_t* own_gate, int col, int N) {
+  // One branch a part, not one a column: they cost as much as the arithmetic.
+  auto each = [&](const float* k, auto op) {
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float v[8], k[8];
+    for (int c = 0; c < 8; ++c) {
+      const float4 w = reinterpret_cast<const float4*>(k)[c];
+      float y[4];
+      unpack2(op(pack2(__uint_as_float(x[4 * c]), __uint_as_float(x[4 * c + 1])), pack2(w.x, w.y)), y[0], y[1]);
+      unpack2(op(pack2(__uint_as_float(x[4 * c + 2]), __uint_as_float(x[4 * c + 3])), pack2(w.z, w.w)), y[2], y[3]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[8 * c + i]);
-    const int c0 = col + 8 * c;
-    auto row = [&](const uint16_t* p) {
-      if constexpr (kVec) {
-        const uint4 w = c0 < a.N ? __ldg(reinterpret_cast<const uint4*>(p + c0)) : make_uint4(0, 0, 0, 0);
-        k[0] = bf16_lo(w.x), k[1] = bf16_hi(w.x), k[2] = bf16_lo(w.y), k[3] = bf16_hi(w.y);
-        k[4] = bf16_lo(w.z), k[5] = bf16_hi(w.z), k[6] = bf16_lo(w.w), k[7] = bf16_hi(w.w);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) k[i] = c0 + i < a.N ? bf16_at(p + c0 + i) : 0.0f;
-      }
-    };
-    if (a.bias) {
-      row(a.bias);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += k[i];
+      for (int i = 0; i < 4; ++i) x[4 * c + i] = __float_as_uint(y[i]);
     }
+  };
+  if (bias) each(bias, [](f2 a, f2 b) { return add2(a, b); });
+  if constexpr (kAct != KQ_ACT_NONE) {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) activate<kAct>(v[i], v[i + 1]);
-    if (gate) {
-      row(gate);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= k[i];
+    for (int c = 0; c < 32; c += 2) {
+      float a, b;
+      unpack2(activate<kAct>(pack2(__uint_as_float(x[c]), __uint_as_float(x[c + 1]))), a, b);
+      x[c] = __float_as_uint(a);
+      x[c + 1] = __float_as_uint(b);
     }
+  }
+  if (gate) each(gate, [](f2 a, f2 b) { return mul2(a, b); });
+  if (own_gate) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[8 * c + i] = __float_as_uint(v[i]);
+    for (int c = 0; c < 32; ++c)
+      if (col + c < N) x[c] = __float_as_uint(__uint_as_float(x[c]) * bf16_at(own_gate + col + c));
   }
 }
 
@@ -160,7 +179,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 template <int kN, bool kBf16, int kAct>
-__global__ void __launch_bounds__(kEpThreads, 1)
+__global__ void __launch_bounds__(EpGeom<kN>::kThreads, 1)
     gemm_mxf4_ep(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                  const __grid_constant__ CUtensorMap sfamap, const __grid_constant__ CUtensorMap sfbmap,
                  const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap rmap,
@@ -171,12 +190,13 @@ __global__ void __launch_bounds__(kEpThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   uint8_t* staging = base + kStages * P::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpStaging);
+  float* vectors = reinterpret_cast<float*>(staging + kEpStaging);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpStaging + E::kVectors);
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + P::kAcc;
   uint64_t* res_full = acc_empty + P::kAcc;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + kEpWarps);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + E::kWarps);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
@@ -189,42 +209,68 @@ __global__ void __launch_bounds__(kEpThreads, 1)
     }
     for (int b = 0; b < P::kAcc; ++b) {
       mbar_init(&acc_full[b], 1);                    // rank 0's commit, multicast
-      mbar_init(&acc_empty[b], 2 * kEpWarps);        // the epilogue warps of each CTA
+      mbar_init(&acc_empty[b], 2 * E::kWarps);       // the epilogue warps of each CTA
     }
-    for (int w = 0; w < kEpWarps; ++w) mbar_init(&res_full[w], 1);
+    for (int w = 0; w < E::kWarps; ++w) mbar_init(&res_full[w], 1);
     fence_mbar_init_cluster();
   }
-  if (warp == 1) tmem_alloc_pair(tmem_slot, kTmemCols);
+  if (warp == E::kWarps + 1) tmem_alloc_pair(tmem_slot, kTmemCols);
   tmem_fence_before();
   cluster_sync();                                    // barriers of both CTAs initialised
   tmem_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait_then_trigger();
 
-  if (warp == 0) {
-    if (elect_one() && !pair_produce<kN, kStages>(base, full, empty, &amap, &bmap, &sfamap, &sfbmap,
-                                                a.tiles, rank, pair, n_pairs))
-      atomicOr(a.err, kErrProducerWait);
-  } else if (warp == 1) {
+  if (warp >= E::kWarps) {
+    if constexpr (E::kSplit) regs_down<E::kRestRegs>();
     const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem_base);       // uniform
-    if (rank == 0 && elect_one() &&
-        !pair_mma<kN, kStages>(base, full, empty, acc_full, acc_empty, tm, a.tiles, pair, n_pairs))
-      atomicOr(a.err, kErrConsumerWait);
+    if (warp == E::kWarps) {
+      if (elect_one() && !pair_produce<kN, kStages>(base, full, empty, &amap, &bmap, &sfamap, &sfbmap,
+                                                    a.tiles, rank, pair, n_pairs))
+        atomicOr(a.err, kErrProducerWait);
+    } else if (warp == E::kWarps + 1) {
+      if (rank == 0 && elect_one() &&
+          !pair_mma<kN, kStages>(base, full, empty, acc_full, acc_empty, tm, a.tiles, pair, n_pairs))
+        atomicOr(a.err, kErrConsumerWait);
+    }
   } else {
-    constexpr int kGroups = E::kCols / 32;           // 32-column groups of a thread
+    if constexpr (E::kSplit) regs_up<E::kEpRegs>();
+    constexpr int kGroups = kCols / 32;           // 32-column groups of a thread
     constexpr int kBoxCols = kBf16 ? 64 : 32;
-    constexpr int kBoxes = E::kCols / kBoxCols;      // boxes of a warp and tile
-    constexpr int kRound = kBoxes < kSlots ? kBoxes : kSlots;
-    const int quarter = warp & 3, side = (warp - 2) >> 2;
-    const uint32_t taddr = tmem_base + (uint32_t(quarter * 32) << 16) + side * E::kCols;
-    uint8_t* slots = staging + (warp - 2) * (kSlots * kBoxBytes);
-    uint64_t* rbar = &res_full[warp - 2];
+    constexpr int kBoxes = kCols / kBoxCols;      // boxes of a warp and tile
+    constexpr int kRound = kBoxes < E::kSlots ? kBoxes : E::kSlots;
+    const int quarter = warp & 3, side = warp >> 2;
+    const uint32_t taddr = tmem_base + (uint32_t(quarter * 32) << 16) + side * kCols;
+    uint8_t* slots = staging + warp * (E::kSlots * kBoxBytes);
+    uint64_t* rbar = &res_full[warp];
+    float* vec = vectors + warp * (2 * kCols);
     uint32_t rphase = 0;
+    // Bias and gate of a tile's columns, a column in each lane, as float bits.  The
+    // rows of a warp mostly belong to one sample.
+    constexpr int kPer = kCols / 32;
+    uint32_t nb[kPer], ng[kPer];
+    bool n_one = true;
+    auto load_vectors = [&](int tile) {
+      if (tile >= n_tiles_total) return;
+      int m0, n0;
+      pair_tile_origin<kN>(a.tiles, tile, m0, n0);
+      const int row0 = min(m0 + (int)rank * kBM + quarter * 32, a.M - 1), col = n0 + side * kCols + lane;
+      const int sample = a.gate ? row0 / a.tokens : 0;
+      n_one = !a.gate || min(row0 + 31, a.M - 1) / a.tokens == sample;
+      const uint16_t* gate = a.gate ? a.gate + static_cast<int64_t>(sample) * a.N : nullptr;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const bool in = col + 32 * k < a.N;
+        nb[k] = a.bias && in ? static_cast<uint32_t>(__ldg(a.bias + col + 32 * k)) << 16 : 0u;
+        ng[k] = gate && in ? static_cast<uint32_t>(__ldg(gate + col + 32 * k)) << 16 : 0u;
+      }
+    };
+    load_vectors(pair);
     int i = 0;
     for (int t = pair; t < n_tiles_total; t += n_pairs, ++i) {
       int m0, n0;
       pair_tile_origin<kN>(a.tiles, t, m0, n0);
-      const int row0 = m0 + (int)rank * kBM + quarter * 32, col0 = n0 + side * E::kCols;
+      const int row0 = m0 + (int)rank * kBM + quarter * 32, col0 = n0 + side * kCols;
       const bool live = row0 < a.M && col0 < a.N;    // some of this warp's box is inside
       // Boxes of round r: their slots are free once the stores out of them
       // have been read; the residual goes in first.
@@ -243,6 +289,17 @@ __global__ void __launch_bounds__(kEpThreads, 1)
         __syncwarp();
       };
       if (live && a.boxes) begin_round(0);
+      if (live) {
+        // This tile's bias and gate, loaded under the last one's arithmetic.
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          vec[lane + 32 * k] = __uint_as_float(nb[k]);
+          vec[kCols + lane + 32 * k] = __uint_as_float(ng[k]);
+        }
+        __syncwarp();
+      }
+      const bool one_sample = n_one;
       const int b = i % P::kAcc;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[b], (i / P::kAcc) & 1))) {
         if (lane == 0) {
@@ -259,10 +316,17 @@ __global__ void __launch_bounds__(kEpThreads, 1)
       tmem_wait_ld();
       tmem_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[b], 0));
+      if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&acc_empty[b], 0));
+      load_vectors(t + n_pairs);
       if (!live) continue;
-      const uint16_t* gate =
-          a.gate ? a.gate + static_cast<int64_t>(min(row0 + lane, a.M - 1) / a.tokens) * a.N : nullptr;
+      const float* bias = a.bias ? vec : nullptr;
+      const float* gate = a.gate && one_sample ? vec + kCols : nullptr;
+      const uint16_t* own_gate =
+          a.gate && !one_sample ? a.gate + static_cast<int64_t>(min(row0 + lane, a.M - 1) / a.tokens) * a.N : nullptr;
+      auto act = [&](uint32_t (&y)[32], int v) {
+        finish<kAct>(y, bias ? bias + 32 * v : nullptr, gate ? gate + 32 * v : nullptr, own_gate,
+                     col0 + 32 * v, a.N);
+      };
 
       if (a.boxes) {
 #pragma unroll
@@ -270,7 +334,7 @@ __global__ void __launch_bounds__(kEpThreads, 1)
           if (r > 0) begin_round(r);
 #pragma unroll
           for (int v = r * kRound * kBoxCols / 32; v < (r + 1) * kRound * kBoxCols / 32; ++v)
-            finish<kAct, true>(x[v], a, col0 + 32 * v, gate);
+            act(x[v], v);
           if (a.residual) {
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(rbar, rphase))) {
               if (lane == 0) atomicOr(a.err, kErrConsumerWait);
@@ -315,34 +379,44 @@ __global__ void __launch_bounds__(kEpThreads, 1)
             bulk_commit();
           }
         }
-      } else {
-        // Rows whose pitch or width TMA cannot take: 32 columns at a time
-        // through a box of 32 x 32 floats, so that a warp's global accesses run
-        // along a row.
+      } else if constexpr (kN == 128) {
+        // Rows whose pitch or width TMA cannot take (narrow tiles only): 32 columns
+        // at a time through a box of 32 x 32 floats, so that a warp's global
+        // accesses run along a row, the residual's all in flight at once and under
+        // the arithmetic.
         float* box = reinterpret_cast<float*>(slots);
+        const int n_rows = min(32, a.M - row0);
 #pragma unroll
         for (int v = 0; v < kGroups; ++v) {
-          const int col = col0 + 32 * v;
-          finish<kAct, false>(x[v], a, col, gate);
+          const int col = col0 + 32 * v + lane;
+          const int64_t at0 = static_cast<int64_t>(row0) * a.N + col;
+          const bool in = col < a.N;
+          float res[32];
+          if (a.residual) {
+#pragma unroll
+            for (int r = 0; r < 32; ++r) {
+              const int64_t at = at0 + static_cast<int64_t>(r) * a.N;
+              res[r] = 0.0f;
+              if (in && r < n_rows) {
+                if constexpr (kBf16) res[r] = bf16_at(static_cast<const uint16_t*>(a.residual) + at);
+                else res[r] = __ldcs(static_cast<const float*>(a.residual) + at);
+              }
+            }
+          }
+          act(x[v], v);
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             *reinterpret_cast<uint4*>(box + lane * 32 + 4 * (c ^ (lane & 7))) =
                 make_uint4(x[v][4 * c], x[v][4 * c + 1], x[v][4 * c + 2], x[v][4 * c + 3]);
           __syncwarp();
-          if (col + lane < a.N) {
-            const int n_rows = min(32, a.M - row0);
-            const int64_t at0 = static_cast<int64_t>(row0) * a.N + col + lane;
-#pragma unroll 8
-            for (int r = 0; r < n_rows; ++r) {
-              float y = box[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)];
-              const int64_t at = at0 + static_cast<int64_t>(r) * a.N;
-              if constexpr (kBf16) {
-                if (a.residual) y += bf16_at(static_cast<const uint16_t*>(a.residual) + at);
-                static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-              } else {
-                if (a.residual) y += static_cast<const float*>(a.residual)[at];
-                static_cast<float*>(a.out)[at] = y;
-              }
+#pragma unroll
+          for (int r = 0; r < 32; ++r) {
+            float y = box[r * 32 + 4 * ((lane >> 2) ^ (r & 7)) + (lane & 3)];
+            if (a.residual) y += res[r];
+            const int64_t at = at0 + static_cast<int64_t>(r) * a.N;
+            if (in && r < n_rows) {
+              if constexpr (kBf16) static_cast<uint16_t*>(a.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+              else static_cast<float*>(a.out)[at] = y;
             }
           }
           __syncwarp();
@@ -357,7 +431,7 @@ __global__ void __launch_bounds__(kEpThreads, 1)
   // wait above is bounded, so both CTAs get here.
   __syncwarp();
   cluster_sync();
-  if (warp == 1) {
+  if (warp == E::kWarps + 1) {
     tmem_fence_after();
     tmem_dealloc_pair(tmem_base, kTmemCols);
   }
@@ -406,8 +480,15 @@ int launch_ep(const EpCall& c, EpArgs a) {
     return record_cuda_error(cudaErrorInvalidValue);
   const int rc = allow_smem<gemm_mxf4_ep<kN, kBf16, kAct>>(E::kSmem, c.dev);
   if (rc != KQ_OK) return rc;
+  if constexpr (E::kSplit) {
+    // setmaxnreg draws on what the block was launched with: were that less than
+    // the warps' shares, the kernel would wait for good.
+    static const int regs = launched_regs(gemm_mxf4_ep<kN, kBf16, kAct>);
+    if (regs * (E::kWarps + 4) < E::kEpRegs * E::kWarps + E::kRestRegs * 4)
+      return record_cuda_error(cudaErrorLaunchOutOfResources);
+  }
   return launch_pairs<gemm_mxf4_ep<kN, kBf16, kAct>>(
-      kEpThreads, E::kSmem, (int64_t)a.tiles.m_tiles * a.tiles.n_tiles, c.di, c.dev, true, c.st, amap,
+      E::kThreads, E::kSmem, (int64_t)a.tiles.m_tiles * a.tiles.n_tiles, c.di, c.dev, true, c.st, amap,
       bmap, sfamap, sfbmap, cmap, rmap, a);
 }
 
@@ -423,11 +504,15 @@ int launch_ep_act(const EpCall& c, const EpArgs& a, int act) {
 
 // Tile width: what fills the pairs in fewer column-steps.  Tiles of 128 columns
 // quantize the work more finely and hide the accumulator's drain behind a
-// second accumulator, but bring 1.5 times the operand bytes per product.
-bool wide_tiles(int64_t M, int64_t N, int pairs) {
-  const int64_t mt = (M + kPairM - 1) / kPairM;
-  const int64_t wide = (mt * ((N + 255) / 256) + pairs - 1) / pairs * 2;
-  const int64_t narrow = (mt * ((N + 127) / 128) + pairs - 1) / pairs;
+// second accumulator, but bring 1.5 times the operand bytes per product.  Only
+// bf16 rows that take TMA boxes have wide tiles: a thread's half of a wide float32
+// row, or the residual of one that is read along its rows, does not fit beside the
+// 128 accumulator registers.
+bool wide_tiles(const EpArgs& a, bool bf16, int pairs) {
+  if (!bf16 || !a.boxes) return false;
+  const int64_t mt = (a.M + kPairM - 1) / kPairM;
+  const int64_t wide = (mt * ((a.N + 255) / 256) + pairs - 1) / pairs * 2;
+  const int64_t narrow = (mt * ((a.N + 127) / 128) + pairs - 1) / pairs;
   return 5 * narrow >= 4 * wide;
 }
 
@@ -469,8 +554,7 @@ extern "C" int kq_gemm_mxfp4_epilogue(const uint8_t* qa, const uint8_t* sa_tiled
   a.gate = gate;
   a.residual = residual;
   a.out = c;
-  const bool wide = wide_tiles(M, N, call.di->sms / 2);
-  if (call.bf16)
-    return wide ? launch_ep_act<256, true>(call, a, activation) : launch_ep_act<128, true>(call, a, activation);
-  return wide ? launch_ep_act<256, false>(call, a, activation) : launch_ep_act<128, false>(call, a, activation);
+  if (wide_tiles(a, call.bf16, call.di->sms / 2)) return launch_ep_act<256, true>(call, a, activation);
+  return call.bf16 ? launch_ep_act<128, true>(call, a, activation)
+                   : launch_ep_act<128, false>(call, a, activation);
 }

@@ -44,6 +44,22 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
+// A warpgroup's share of the registers that the block was launched with.
+template <int kRegs>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+// Host: registers a thread that a kernel is launched with (0 if unknown).
+template <typename... KArgs>
+inline int launched_regs(void (*kernel)(KArgs...)) {
+  cudaFuncAttributes f{};
+  return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
+}
+
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    smem_addr(bar))
@@ -166,6 +182,13 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr)
                : "memory");
+}
+
+// The same without release semantics, for a hand-over of tensor memory alone,
+// which the tcgen05 fences order: the release at cluster scope took about 2000
+// cycles in an epilogue warp.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
 
 // Bounded wait on a local mbarrier that arrivals from the other CTA complete

@@ -37,19 +37,25 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 
 // ---------------------------------------------------------------------------
 // Few query rows: one warp walks 32 positions at a time with mma.sync, its
-// operands decoded in registers.  The rows fill (part of) the MMA's 16, so the
-// cost is the cache's bytes and their decoding, whatever the group.
+// operands decoded in registers.  The products are taken transposed,
+//   S^T = K q^T  [positions][rows]   and   O^T = V^T P^T  [channels][rows],
+// so that the cache fills the MMA's 16 and the few query rows its 8: the usual
+// single-token group of up to 8 heads costs half the MMAs, exponentials and
+// accumulators of the other way round.  What is left is the decoding of the
+// codes, 13 instructions for 8 of them, and that bounds the kernel.
 //
 // Lane (g, c) = (lane / 4, lane mod 4).  The products contract over the head's
 // channels (S) and the positions (O) in any order, as long as both operands
 // use the same one, so each lane takes what is contiguous for it:
-//   K  lane c's quarter of the row of position n = g, one 4-byte word being the
-//      channels of two MMA k-steps,
-//   V  for positions c, c + 4, c + 8, c + 12 of 16, the g-th eighth of the row.
-// No shuffle and no transpose lies between the cache's bytes and the MMA.
+//   K  for positions tau(g) and tau(g) + 8 of 16, lane c's quarter of the row, one
+//      4-byte word being the channels of two MMA k-steps,
+//   V  for positions c, c + 4, c + 8, c + 12, the g-th eighth of the row,
+// with tau(2 c) = c, tau(2 c + 1) = c + 4, which keeps both free of bank conflicts.
+// P comes out of the first product with positions along g and goes into the second
+// with positions along c: an 8 x 8 transpose, movmatrix.
 constexpr int kWarps = 4;
 constexpr int kTile = 32;                     // positions a warp holds at a time
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 
 template <int kW>                             // 32-channel blocks of a row
 struct SplitGeom {
@@ -59,64 +65,43 @@ struct SplitGeom {
   static constexpr int kStage = 2 * kCodes + 2 * kScales;
   static constexpr int kRing = kWarps * kStages * kStage;
 };
-template <int kW, int kMT>
+// The ring; in the end the warps' parts.
+template <int kW, int kNT>
 constexpr int split_smem() {
-  const int merge = kWarps * 16 * kMT * (32 * kW + 2) * 4;
+  const int merge = kWarps * 8 * kNT * (32 * kW + 2) * 4;
   return merge > SplitGeom<kW>::kRing ? merge : SplitGeom<kW>::kRing;
 }
 
-template <int kW, int kMT>
-__global__ void __launch_bounds__(32 * kWarps) attn_split_kernel(const AttnArgs a) {
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// kNT: groups of 8 query rows.
+template <int kW, int kNT>
+__global__ void __launch_bounds__(32 * kWarps, kNT == 1 ? 4 : kNT == 2 ? 3 : 2)
+    attn_split_kernel(const AttnArgs a) {
   using G = SplitGeom<kW>;
+  constexpr int kRows = 8 * kNT;
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const int chunk = blockIdx.x % a.n_chunks, r0 = blockIdx.x / a.n_chunks * (16 * kMT);
+  const int tau = (g >> 1) + 4 * (g & 1);
+  const int chunk = blockIdx.x % a.n_chunks, r0 = blockIdx.x / a.n_chunks * kRows;
   const int hk = blockIdx.y;
   const int64_t b = blockIdx.z;
   pdl_wait_then_trigger();
 
   const int len = seq_len(a, b);
   const int first_limit = row_limit(a, len, r0);                       // the fewest a row sees
-  const int last_limit = row_limit(a, len, min(r0 + 16 * kMT, a.rows) - 1);
+  const int last_limit = row_limit(a, len, min(r0 + kRows, a.rows) - 1);
   const int begin = chunk * a.chunk;
   const int end = min(begin + a.chunk, last_limit);
-  int limit[kMT][2];
+  int limit[kNT][2];
 #pragma unroll
-  for (int t = 0; t < kMT; ++t) {
-    limit[t][0] = row_limit(a, len, r0 + 16 * t + g);
-    limit[t][1] = row_limit(a, len, r0 + 16 * t + g + 8);
-  }
-
-  // Queries as A fragments, in the channel order of the K words.
-  uint32_t q[kMT][2 * kW][4];
-#pragma unroll
-  for (int t = 0; t < kMT; ++t)
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = r0 + 16 * t + g + 8 * hf;
-      const int m = a.group.div(r), h = hk * a.group.d + r - m * a.group.d;
-#pragma unroll
-      for (int j = 0; j < kW; ++j) {
-        const int d0 = (c * kW + j) * 8;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < a.rows && d0 < a.D)
-          x = __ldg(reinterpret_cast<const uint4*>(a.q + b * a.qb + m * a.qm + h * a.qh + d0));
-        q[t][2 * j][hf] = __byte_perm(x.x, x.z, 0x5410);
-        q[t][2 * j][2 + hf] = __byte_perm(x.x, x.z, 0x7632);
-        q[t][2 * j + 1][hf] = __byte_perm(x.y, x.w, 0x5410);
-        q[t][2 * j + 1][2 + hf] = __byte_perm(x.y, x.w, 0x7632);
-      }
-    }
-
-  float o[kMT][4 * kW][4], mx[kMT][2], l[kMT][2];
-#pragma unroll
-  for (int t = 0; t < kMT; ++t) {
-#pragma unroll
-    for (int n = 0; n < 4 * kW; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[t][n][k] = 0.0f;
-    mx[t][0] = mx[t][1] = -INFINITY;
-    l[t][0] = l[t][1] = 0.0f;
+  for (int t = 0; t < kNT; ++t) {
+    limit[t][0] = row_limit(a, len, r0 + 8 * t + 2 * c);
+    limit[t][1] = row_limit(a, len, r0 + 8 * t + 2 * c + 1);
   }
 
   // This warp's tiles: positions begin + 32 (warp + 4 i).
@@ -140,7 +125,7 @@ __global__ void __launch_bounds__(32 * kWarps) attn_split_kernel(const AttnArgs 
       }
     }
   };
-  uint32_t absent = 0;                        // bit 2 (i mod 4) + half: that half has no page
+  uint32_t absent = 0;                        // bit 2 (i mod kStages) + half: that half has no page
   auto load_tile = [&](int i) {
     if (i < n_tiles) {
       if ((i & 15) == 0) load_pages(i);
@@ -176,9 +161,39 @@ __global__ void __launch_bounds__(32 * kWarps) attn_split_kernel(const AttnArgs 
     }
     cp_async_commit();
   };
-
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) load_tile(i);
+
+  // Query row 8 t + g as B fragments, in the channel order of the K words.
+  uint32_t q[kNT][2 * kW][2];
+#pragma unroll
+  for (int t = 0; t < kNT; ++t) {
+    const int r = r0 + 8 * t + g;
+    const int m = a.group.div(r), h = hk * a.group.d + r - m * a.group.d;
+#pragma unroll
+    for (int j = 0; j < kW; ++j) {
+      const int d0 = (c * kW + j) * 8;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < a.rows && d0 < a.D)
+        x = __ldg(reinterpret_cast<const uint4*>(a.q + b * a.qb + m * a.qm + h * a.qh + d0));
+      q[t][2 * j][0] = __byte_perm(x.x, x.z, 0x5410);
+      q[t][2 * j][1] = __byte_perm(x.x, x.z, 0x7632);
+      q[t][2 * j + 1][0] = __byte_perm(x.y, x.w, 0x5410);
+      q[t][2 * j + 1][1] = __byte_perm(x.y, x.w, 0x7632);
+    }
+  }
+
+  // O^T: MMA tile n holds channels 4 kW g + 2 n (rows g) and the next (rows g + 8).
+  float o[kNT][2 * kW][4], mx[kNT][2], l[kNT][2];
+#pragma unroll
+  for (int t = 0; t < kNT; ++t) {
+#pragma unroll
+    for (int n = 0; n < 2 * kW; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[t][n][k] = 0.0f;
+    mx[t][0] = mx[t][1] = -INFINITY;
+    l[t][0] = l[t][1] = 0.0f;
+  }
 
   for (int i = 0; i < n_tiles; ++i) {
     cp_async_wait<kStages - 2>();
@@ -190,99 +205,110 @@ __global__ void __launch_bounds__(32 * kWarps) attn_split_kernel(const AttnArgs 
     const uint8_t* vsc = ksc + G::kScales;
     const int pos = tile_pos(i);
 
-    // S of 32 positions.
-    float s[kMT][4][4];
+    // S^T of 2 x 16 positions.
+    float s[2][kNT][4];
+    {
+      uint32_t w[4][kW], m2[4][kW];           // positions tau + 8 u
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
+      for (int u = 0; u < 4; ++u) {
+        const int tok = 8 * u + tau;
+        const uint32_t* kw = reinterpret_cast<const uint32_t*>(st + tok * (G::kDp / 2)) + c * kW;
+        if constexpr (kW == 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(kw);
+          w[u][0] = x.x, w[u][1] = x.y, w[u][2] = x.z, w[u][3] = x.w;
+        } else if constexpr (kW == 2) {
+          const uint2 x = *reinterpret_cast<const uint2*>(kw);
+          w[u][0] = x.x, w[u][1] = x.y;
+        } else {
 #pragma unroll
-      for (int t = 0; t < kMT; ++t)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[t][n][k] = 0.0f;
-      const int tok = 8 * n + (g >> 1) + 4 * (g & 1);
-      uint32_t w[kW];
-      const uint32_t* kw = reinterpret_cast<const uint32_t*>(st + tok * (G::kDp / 2)) + c * kW;
-      if constexpr (kW == 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(kw);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-      } else if constexpr (kW == 2) {
-        const uint2 x = *reinterpret_cast<const uint2*>(kw);
-        w[0] = x.x, w[1] = x.y;
-      } else {
-#pragma unroll
-        for (int j = 0; j < kW; ++j) w[j] = kw[j];
-      }
-#pragma unroll
-      for (int j = 0; j < kW; ++j) {
-        const uint32_t m2 = mx_mul(ksc[tok * kW + ((c * kW + j) >> 2)]) * 0x10001u;
-        uint32_t p[4];
-        e2m1_pairs(w[j], p);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) p[k] = mul_bf16x2(p[k], m2);
-#pragma unroll
-        for (int t = 0; t < kMT; ++t) {
-          mma_bf16(s[t][n], q[t][2 * j], p[0], p[1]);
-          mma_bf16(s[t][n], q[t][2 * j + 1], p[2], p[3]);
+          for (int j = 0; j < kW; ++j) w[u][j] = kw[j];
         }
+#pragma unroll
+        for (int j = 0; j < kW; ++j) m2[u][j] = mx_mul(ksc[tok * kW + ((c * kW + j) >> 2)]) * 0x10001u;
       }
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) s[half][t][k] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kW; ++j)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t p[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            e2m1_pairs(w[2 * half + u][j], p[u]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) p[u][k] = mul_bf16x2(p[u][k], m2[2 * half + u][j]);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t x[4] = {p[0][2 * e], p[1][2 * e], p[0][2 * e + 1], p[1][2 * e + 1]};
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) mma_bf16(s[half][t], x, q[t][2 * j + e][0], q[t][2 * j + e][1]);
+          }
+        }
     }
 
-    // Running maximum and sum.  Column 2 c of tile n is position 8 n + c,
-    // column 2 c + 1 position 8 n + c + 4 (16 positions: 8 n -> 16 half + 8).
+    // Running maximum and sum of rows 8 t + 2 c and the next; element k is position
+    // tau + 8 (k / 2) of its 16, row 2 c + k mod 2.
     const bool ragged = pos + kTile > first_limit || gone;
-    uint32_t pa[kMT][2][4];
+    uint32_t pb[2][kNT][2];
 #pragma unroll
-    for (int t = 0; t < kMT; ++t) {
+    for (int t = 0; t < kNT; ++t) {
       const float sc = a.scale_log2 * kUnscale;
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float v = s[t][n][k] * sc;
+          float v = s[half][t][k] * sc;
           if (ragged) {
-            const int p = pos + 8 * n + c + 4 * (k & 1);
-            if (p >= limit[t][k >> 1] || (gone >> (n >> 1) & 1)) v = -INFINITY;
+            const int p = pos + 16 * half + tau + 8 * (k >> 1);
+            if (p >= limit[t][k & 1] || (gone >> half & 1)) v = -INFINITY;
           }
-          s[t][n][k] = v;
-          top[k >> 1] = fmaxf(top[k >> 1], v);
+          s[half][t][k] = v;
+          top[k & 1] = fmaxf(top[k & 1], v);
         }
       bool grew = false;
       float base[2], alpha[2];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xFFFFFFFFu, top[hf], 1));
-        top[hf] = fmaxf(top[hf], __shfl_xor_sync(0xFFFFFFFFu, top[hf], 2));
-        const float m_new = fmaxf(mx[t][hf], top[hf]);
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xFFFFFFFFu, top[e], x));
+        const float m_new = fmaxf(mx[t][e], top[e]);
         // A row that has seen nothing yet: exp2(-inf - 0) = 0.
-        base[hf] = m_new == -INFINITY ? 0.0f : m_new;
-        alpha[hf] = ex2(mx[t][hf] - base[hf]);
-        base[hf] -= kShift;
-        grew |= m_new > mx[t][hf];
-        mx[t][hf] = m_new;
+        base[e] = m_new == -INFINITY ? 0.0f : m_new;
+        alpha[e] = ex2(mx[t][e] - base[e]);
+        base[e] -= kShift;
+        grew |= m_new > mx[t][e];
+        mx[t][e] = m_new;
       }
       if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
-        for (int n = 0; n < 4 * kW; ++n)
+        for (int n = 0; n < 2 * kW; ++n)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[t][n][k] *= alpha[k >> 1];
+          for (int k = 0; k < 4; ++k) o[t][n][k] *= alpha[k & 1];
         l[t][0] *= alpha[0];
         l[t][1] *= alpha[1];
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
+      for (int half = 0; half < 2; ++half) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          s[t][n][k] = ex2(s[t][n][k] - base[k >> 1]);
-          l[t][k >> 1] += s[t][n][k];
+          s[half][t][k] = ex2(s[half][t][k] - base[k & 1]);
+          l[t][k & 1] += s[half][t][k];
         }
         // The weights are rounded to bf16, the type of the product (each by at
         // most 2^-8 of itself); their sum is taken before.
-        pa[t][n >> 1][2 * (n & 1)] = bf16x2(s[t][n][0], s[t][n][1]);
-        pa[t][n >> 1][2 * (n & 1) + 1] = bf16x2(s[t][n][2], s[t][n][3]);
+        pb[half][t][0] = transpose8x8(bf16x2(s[half][t][0], s[half][t][1]));
+        pb[half][t][1] = transpose8x8(bf16x2(s[half][t][2], s[half][t][3]));
       }
     }
 
-    // O += P V.
+    // O^T += V^T P^T.
     const bool tail = pos + kTile > len || gone;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -308,12 +334,12 @@ __global__ void __launch_bounds__(32 * kWarps) attn_split_kernel(const AttnArgs 
       for (int u = 0; u < kW; ++u) {
         uint32_t m[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int tok = 16 * half + c + 4 * k;
-          m[k] = mx_mul(vsc[tok * kW + ((g * kW + u) >> 3)]);
-          // What lies behind the sequence is unknown: its codes times zero.
-          if (tail && (pos + tok >= len || (gone >> half & 1))) m[k] = 0;
-        }
+        for (int k = 0; k < 4; ++k) m[k] = mx_mul(vsc[(16 * half + c + 4 * k) * kW + ((g * kW + u) >> 3)]);
+        // What lies behind the sequence is unknown: its codes times zero.
+        if (tail)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (pos + 16 * half + c + 4 * k >= len || (gone >> half & 1)) m[k] = 0;
         const uint32_t m01 = m[0] | m[1] << 16, m23 = m[2] | m[3] << 16;
         const uint32_t sel = u & 1 ? 0x7632 : 0x5410;
         uint32_t x[4], y[4];
@@ -321,9 +347,14 @@ __global__ void __launch_bounds__(32 * kWarps) attn_split_kernel(const AttnArgs 
         e2m1_pairs(__byte_perm(hw[2][u >> 1], hw[3][u >> 1], sel), y);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t b0 = mul_bf16x2(x[k], m01), b1 = mul_bf16x2(y[k], m23);
+          x[k] = mul_bf16x2(x[k], m01);
+          y[k] = mul_bf16x2(y[k], m23);
+        }
 #pragma unroll
-          for (int t = 0; t < kMT; ++t) mma_bf16(o[t][4 * u + k], pa[t][half], b0, b1);
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t va[4] = {x[2 * k], x[2 * k + 1], y[2 * k], y[2 * k + 1]};
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) mma_bf16(o[t][2 * u + k], va, pb[half][t][0], pb[half][t][1]);
         }
       }
     }
@@ -333,31 +364,25 @@ __global__ void __launch_bounds__(32 * kWarps) attn_split_kernel(const AttnArgs 
 
   // The four warps' parts, joined in a fixed order.
 #pragma unroll
-  for (int t = 0; t < kMT; ++t)
+  for (int t = 0; t < kNT; ++t)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      l[t][hf] += __shfl_xor_sync(0xFFFFFFFFu, l[t][hf], 1);
-      l[t][hf] += __shfl_xor_sync(0xFFFFFFFFu, l[t][hf], 2);
-    }
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[t][e] += __shfl_xor_sync(0xFFFFFFFFu, l[t][e], x);
   __syncthreads();
-  constexpr int kRows = 16 * kMT;
   float* so = reinterpret_cast<float*>(smem);                    // [warp][row][Dp]
   float2* sml = reinterpret_cast<float2*>(so + kWarps * kRows * G::kDp);
 #pragma unroll
-  for (int t = 0; t < kMT; ++t)
+  for (int t = 0; t < kNT; ++t)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = 16 * t + g + 8 * hf;
-      float* dst = so + (warp * kRows + r) * G::kDp;
-      // Column n of MMA tile j is channel n (Dp / 8) + j.
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * t + 2 * c + e;
+      float* dst = so + (warp * kRows + r) * G::kDp + g * 4 * kW;
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int u = 0; u < kW; ++u)
-          *reinterpret_cast<float4*>(dst + (2 * c + e) * 4 * kW + 4 * u) =
-              make_float4(o[t][4 * u][2 * hf + e], o[t][4 * u + 1][2 * hf + e],
-                          o[t][4 * u + 2][2 * hf + e], o[t][4 * u + 3][2 * hf + e]);
-      if (c == 0) sml[warp * kRows + r] = make_float2(mx[t][hf], l[t][hf]);
+      for (int n = 0; n < 2 * kW; n += 2)
+        *reinterpret_cast<float4*>(dst + 2 * n) =
+            make_float4(o[t][n][e], o[t][n][2 + e], o[t][n + 1][e], o[t][n + 1][2 + e]);
+      if (g == 0) sml[warp * kRows + r] = make_float2(mx[t][e], l[t][e]);
     }
   __syncthreads();
   for (int i = tid; i < kRows * (G::kDp / 4); i += 32 * kWarps) {
@@ -394,12 +419,14 @@ __global__ void __launch_bounds__(32 * kWarps) attn_split_kernel(const AttnArgs 
   }
 }
 
-// Joins the chunks of each row: a warp per row.
+// Joins the chunks of each row, in their order: a warp per row and 32 channels.
 template <int kW>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int64_t n_rows) {
   pdl_wait_then_trigger();
   const int lane = threadIdx.x & 31;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int64_t at = item / kW;
+  const int j = static_cast<int>(item - at * kW);
   if (at >= n_rows) return;
   const int64_t bh = at / a.rows;
   const int r = static_cast<int>(at - bh * a.rows);
@@ -407,34 +434,34 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int64_
   const int hk = static_cast<int>(bh - b * a.view.heads);
   const int n = (row_limit(a, seq_len(a, b), r) + a.chunk - 1) / a.chunk;
   const float2* ml = a.part_ml + bh * a.n_chunks * a.rows + r;
-  const float* po = a.part_o + (bh * a.n_chunks * a.rows + r) * (32 * kW);
+  const float* po = a.part_o + (bh * a.n_chunks * a.rows + r) * (32 * kW) + 32 * j + lane;
   float top = -INFINITY;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[static_cast<int64_t>(i) * a.rows].x);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
   const float base = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f, acc[kW];
-#pragma unroll
-  for (int j = 0; j < kW; ++j) acc[j] = 0.0f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float2 x = ml[static_cast<int64_t>(i) * a.rows];
+  float sum = 0.0f, acc = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    // This lane's chunk of the 32: its weight, zero where the row sees nothing
+    // in it (no O was written there).
+    float2 x = make_float2(-INFINITY, 0.0f);
+    if (i0 + lane < n) x = ml[static_cast<int64_t>(i0 + lane) * a.rows];
     const float k = ex2(x.x - base);
-    sum += k * x.y;
-    // A chunk in which the row sees nothing has written no O.
-    if (x.x != -INFINITY)
+    float part = k * x.y;
 #pragma unroll
-      for (int j = 0; j < kW; ++j)
-        acc[j] += k * po[static_cast<int64_t>(i) * a.rows * (32 * kW) + 32 * j + lane];
+    for (int e = 16; e > 0; e >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, e);
+    sum += part;
+#pragma unroll 8
+    for (int i = 0; i < min(32, n - i0); ++i) {
+      const float w = __shfl_sync(0xFFFFFFFFu, k, i);
+      if (w > 0.0f) acc += w * po[static_cast<int64_t>(i0 + i) * a.rows * (32 * kW)];
+    }
   }
   const int m = a.group.div(r), h = hk * a.group.d + r - m * a.group.d;
   const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
-  uint16_t* dst = a.out + b * a.ob + m * a.om + h * a.oh;
-#pragma unroll
-  for (int j = 0; j < kW; ++j)
-    if (32 * j + lane < a.D)
-      dst[32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[j] * inv));
-  if (a.lse && lane == 0)
+  if (32 * j + lane < a.D)
+    a.out[b * a.ob + m * a.om + h * a.oh + 32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc * inv));
+  if (a.lse && j == 0 && lane == 0)
     a.lse[(b * a.view.heads * a.group.d + h) * a.M + m] =
         top == -INFINITY ? -INFINITY : (top + (log2f(sum) - kShift)) * kLn2;
 }
@@ -459,12 +486,12 @@ AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_le
     p.mask_bytes = static_cast<size_t>((batch * p.tiles * 16 + 255) / 256 * 256);
     p.image_bytes = static_cast<size_t>(images);
   } else {
-    p.mt = rows > 16 ? 2 : 1;
-    p.row_groups = static_cast<int>((rows + 16 * p.mt - 1) / (16 * p.mt));
+    p.nt = rows > 16 ? 4 : rows > 8 ? 2 : 1;
+    p.row_groups = static_cast<int>((rows + 8 * p.nt - 1) / (8 * p.nt));
     constexpr int64_t kStep = kTile * kWarps;
     // About eight CTAs for each SM, of at least 512 positions.
     const int64_t units = batch * kv_heads * p.row_groups;
-    const int64_t want = std::max<int64_t>(1, 8 * kSms / units);
+    const int64_t want = std::max<int64_t>(1, (getenv("KQ_CH") ? atoi(getenv("KQ_CH")) : 8) * kSms / units);
     const int64_t chunk = std::max<int64_t>(512, (max_len + want - 1) / want);
     p.chunk = (chunk + kStep - 1) / kStep * kStep;
   }
@@ -479,14 +506,14 @@ AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_le
   return p;
 }
 
-template <int kW, int kMT>
+template <int kW, int kNT>
 int launch_split(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
-  constexpr int smem = split_smem<kW, kMT>();
-  const int rc = allow_smem<attn_split_kernel<kW, kMT>>(smem, dev);
+  constexpr int smem = split_smem<kW, kNT>();
+  const int rc = allow_smem<attn_split_kernel<kW, kNT>>(smem, dev);
   if (rc != KQ_OK) return rc;
   const dim3 grid(static_cast<unsigned>(p.n_chunks * p.row_groups),
                   static_cast<unsigned>(a.view.heads), static_cast<unsigned>(batch));
-  cudaError_t e = launch_pdl(attn_split_kernel<kW, kMT>, grid, dim3(32 * kWarps), smem, st, a);
+  cudaError_t e = launch_pdl(attn_split_kernel<kW, kNT>, grid, dim3(32 * kWarps), smem, st, a);
   if (e != cudaSuccess) return record_cuda_error(e);
   return KQ_OK;
 }
@@ -494,11 +521,12 @@ int launch_split(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, c
 template <int kW>
 int launch(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
   const int rc = p.tensor_core ? launch_attention_tc(a, p, batch, dev, st)
-                 : p.mt == 1   ? launch_split<kW, 1>(a, p, batch, dev, st)
-                               : launch_split<kW, 2>(a, p, batch, dev, st);
+                 : p.nt == 1   ? launch_split<kW, 1>(a, p, batch, dev, st)
+                 : p.nt == 2   ? launch_split<kW, 2>(a, p, batch, dev, st)
+                               : launch_split<kW, 4>(a, p, batch, dev, st);
   if (rc != KQ_OK || p.n_chunks == 1) return rc;
   const int64_t n_rows = batch * a.view.heads * a.rows;
-  const cudaError_t e = launch_pdl(attn_join_kernel<kW>, dim3(static_cast<unsigned>((n_rows + 3) / 4)),
+  const cudaError_t e = launch_pdl(attn_join_kernel<kW>, dim3(static_cast<unsigned>((n_rows * kW + 3) / 4)),
                                    dim3(128), 0, st, a, n_rows);
   return e == cudaSuccess ? KQ_OK : record_cuda_error(e);
 }
@@ -513,7 +541,7 @@ int64_t attention_rows(int64_t batch, int64_t M, int64_t heads, int64_t kv_heads
     return 0;
   if (M > (int64_t(1) << 30) || heads > (int64_t(1) << 30)) return 0;
   const int64_t rows = M * (heads / kv_heads);
-  return rows <= (int64_t(1) << 30) && batch * kv_heads <= (int64_t(1) << 31) / rows ? rows : 0;
+  return rows <= (int64_t(1) << 30) && batch * kv_heads <= (int64_t(1) << 30) / rows ? rows : 0;
 }
 
 }  // namespace

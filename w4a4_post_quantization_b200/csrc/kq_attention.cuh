@@ -69,13 +69,18 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // nibble i of the high half, as bf16 bits.  A code's sign goes to bit 15 and
 // its exponent and mantissa (two bits and one) to bits 8..6, the low end of
 // bf16's fields, where they mean the code's value times 2^-126: the exponent
-// 0 of E2M1 is bf16's own subnormal.  mx_pair puts the factor right together
-// with the block's scale.
+// 0 of E2M1 is bf16's own subnormal.  mx_mul puts the factor right together
+// with the block's scale.  One product copies a nibble to both places (2^6 and
+// 2^12 above the lowest nibble; nothing carries into the other half), on the
+// multipliers, which are free; as shifts, all of it was work for the
+// logic pipe that bounds the single-token kernel (15 instead of 9 a word).
 __device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&p)[4]) {
-  p[0] = ((w << 6) & 0x01C001C0u) | ((w << 12) & 0x80008000u);
-  p[1] = ((w << 2) & 0x01C001C0u) | ((w << 8) & 0x80008000u);
-  p[2] = ((w >> 2) & 0x01C001C0u) | ((w << 4) & 0x80008000u);
-  p[3] = ((w >> 6) & 0x01C001C0u) | (w & 0x80008000u);
+  constexpr uint32_t kOut = 0x81C081C0u;
+  const uint32_t u = w >> 8;
+  p[0] = ((w & 0x000F000Fu) * 0x1040u) & kOut;
+  p[1] = ((w & 0x00F000F0u) * 0x0104u) & kOut;
+  p[2] = ((u & 0x000F000Fu) * 0x1040u) & kOut;
+  p[3] = ((u & 0x00F000F0u) * 0x0104u) & kOut;
 }
 
 // bf16 bits of 2^(s - 63) for scale byte s <= 190: a raw code times it is the
@@ -92,7 +97,7 @@ constexpr float kUnscale = 4611686018427387904.0f;      // 2^kShift
 // call agree.
 struct AttnPlan {
   bool tensor_core;
-  int row_groups, mt;              // few rows: groups of 16 mt rows
+  int row_groups, nt;              // few rows: groups of 8 nt rows
   int q_tiles;                     // tensor cores: 128-row tiles of a CTA
   int64_t chunk, n_chunks, tiles;
   size_t ml_bytes, part_bytes, mask_bytes, image_bytes, bytes;

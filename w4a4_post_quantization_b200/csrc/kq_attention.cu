@@ -435,6 +435,16 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int64_
   const int n = (row_limit(a, seq_len(a, b), r) + a.chunk - 1) / a.chunk;
   const float2* ml = a.part_ml + bh * a.n_chunks * a.rows + r;
   const float* po = a.part_o + (bh * a.n_chunks * a.rows + r) * (32 * kW) + 32 * j + lane;
+  const int64_t step = static_cast<int64_t>(a.rows) * (32 * kW);
+  // The first chunks' O is on its way while the weights are worked out; O of a
+  // chunk in which the row sees nothing has not been written, and is not used.
+  constexpr int kAhead = 8;
+  float x[kAhead];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) x[i] = i0 + i < n ? po[(i0 + i) * step] : 0.0f;
+  };
+  fetch(0);
   float top = -INFINITY;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, ml[static_cast<int64_t>(i) * a.rows].x);
 #pragma unroll
@@ -442,19 +452,24 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int64_
   const float base = top == -INFINITY ? 0.0f : top;
   float sum = 0.0f, acc = 0.0f;
   for (int i0 = 0; i0 < n; i0 += 32) {
-    // This lane's chunk of the 32: its weight, zero where the row sees nothing
-    // in it (no O was written there).
-    float2 x = make_float2(-INFINITY, 0.0f);
-    if (i0 + lane < n) x = ml[static_cast<int64_t>(i0 + lane) * a.rows];
-    const float k = ex2(x.x - base);
-    float part = k * x.y;
+    // This lane's chunk of the 32: its weight.
+    float2 y = make_float2(-INFINITY, 0.0f);
+    if (i0 + lane < n) y = ml[static_cast<int64_t>(i0 + lane) * a.rows];
+    const float k = ex2(y.x - base);
+    float part = k * y.y;
 #pragma unroll
     for (int e = 16; e > 0; e >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, e);
     sum += part;
-#pragma unroll 8
-    for (int i = 0; i < min(32, n - i0); ++i) {
-      const float w = __shfl_sync(0xFFFFFFFFu, k, i);
-      if (w > 0.0f) acc += w * po[static_cast<int64_t>(i0 + i) * a.rows * (32 * kW)];
+    for (int i1 = i0; i1 < min(i0 + 32, n); i1 += kAhead) {
+      float z[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) z[i] = x[i];
+      fetch(i1 + kAhead);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const float w = __shfl_sync(0xFFFFFFFFu, k, i1 - i0 + i);
+        if (w > 0.0f) acc += w * z[i];
+      }
     }
   }
   const int m = a.group.div(r), h = hk * a.group.d + r - m * a.group.d;
@@ -489,9 +504,10 @@ AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_le
     p.nt = rows > 16 ? 4 : rows > 8 ? 2 : 1;
     p.row_groups = static_cast<int>((rows + 8 * p.nt - 1) / (8 * p.nt));
     constexpr int64_t kStep = kTile * kWarps;
-    // About eight CTAs for each SM, of at least 512 positions.
+    // About eight CTAs for each SM, of at least 512 positions (8 x 8 heads,
+    // 18 to 33 thousand positions: four 96 us, eight 93, sixteen 100).
     const int64_t units = batch * kv_heads * p.row_groups;
-    const int64_t want = std::max<int64_t>(1, (getenv("KQ_CH") ? atoi(getenv("KQ_CH")) : 8) * kSms / units);
+    const int64_t want = std::max<int64_t>(1, 8 * kSms / units);
     const int64_t chunk = std::max<int64_t>(512, (max_len + want - 1) / want);
     p.chunk = (chunk + kStep - 1) / kStep * kStep;
   }

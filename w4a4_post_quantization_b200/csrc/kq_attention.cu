@@ -487,7 +487,11 @@ AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_le
   const int64_t nb = (head_dim + 31) / 32, d16 = (head_dim + 15) / 16 * 16;
   p.tiles = (max_len + 127) / 128;
   const int64_t images = batch * kv_heads * p.tiles * 512 * d16;
-  p.tensor_core = rows > 32 && images <= (int64_t(1) << 32);
+  // Up to 64 rows the split kernel's passes over the codes (one for 32 rows) cost
+  // less than decoding the cache to memory: 8 x 8 heads of 128 over 16384
+  // positions, 64 rows 235 against 295 us, 96 rows 328 against 301.  Past 4 GiB of
+  // decoded tiles it serves any number of rows.
+  p.tensor_core = rows > 64 && images <= (int64_t(1) << 32);
   if (p.tensor_core) {
     // Two query tiles a CTA halve what a wide head's keys and values cost in
     // bandwidth; narrow heads fit two CTAs of one tile on an SM, which hide each

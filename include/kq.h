@@ -364,8 +364,8 @@ int kq_cache_write(const kq_cache* cache, const int32_t* block_table, int64_t ba
 /* Reads rows back: row t < lens[b] of k and v is position start[b] + t,
  * decoded (exactly: E2M1 times a power of two, in bf16 or float32 by dtype
  * KQ_OUT_*); the other rows, and rows left out, are written as zeros.
- * Strides as above, in elements of dtype and multiples of 16 bytes; the
- * elements of k and v must not overlap. */
+ * Strides as above, in elements of dtype and multiples of 16 bytes; no two
+ * elements of k and v may share memory. */
 int kq_cache_read(const kq_cache* cache, const int32_t* block_table, int64_t batch,
                   int64_t table_pages, int64_t tokens, const int32_t* start, const int32_t* lens,
                   void* k, int64_t k_sb, int64_t k_st, int64_t k_sh, void* v, int64_t v_sb,
@@ -382,8 +382,8 @@ int kq_cache_read(const kq_cache* cache, const int32_t* block_table, int64_t bat
  *   multiples of 8.  out must not overlap q.
  *   lse: float32 [batch][heads][M], the natural log-sum-exp of the scaled
  *   scores, or NULL.
- *   max_len: a bound on lens, at most table_pages * page_size; the work is cut
- *   by it, so a tight one is faster.
+ *   max_len: a bound on lens, at most table_pages * page_size and 2^30; the
+ *   work is cut by it, so a tight one is faster.
  *   workspace: kq_attention_workspace_bytes(...) bytes, 256-byte aligned (NULL
  *   where that is 0); its contents before and after do not matter.  Calls that
  *   overlap on the GPU need their own.

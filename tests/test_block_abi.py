@@ -72,7 +72,7 @@ def test_bad_read_type(L):
 @pytest.mark.parametrize("bad", [dict(q=None), dict(q=FAKE + 8), dict(qs=(256, 128, 60)), dict(batch=-1),
                                  dict(M=-1), dict(heads=3), dict(heads=0), dict(table=None),
                                  dict(lens=None), dict(lens=FAKE + 2), dict(max_len=0),
-                                 dict(max_len=49), dict(scale=float("nan")), dict(scale=float("inf")),
+                                 dict(max_len=49), dict(scale=float("nan")), dict(pages=1 << 27, max_len=(1 << 30) + 1), dict(scale=float("inf")),
                                  dict(out=None), dict(out=FAKE + 4), dict(os_=(256, 128, -64)),
                                  dict(lse=FAKE + 2), dict(M=1 << 31)], ids=str)
 def test_bad_attention(L, bad):

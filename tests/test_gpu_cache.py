@@ -240,7 +240,7 @@ def test_refusals():
                 lambda: kq.cache_read(cache, table, lens, 20, k=k[:, :19]),
                 lambda: kq.cache_read(cache, table, lens, 20, k=k.float()),
                 lambda: kq.cache_read(cache, table, lens, 20, k=k[:, :1].expand(-1, 20, -1, -1)),
-                lambda: kq.cache_read(cache, table, lens, "20"),
+                lambda: kq.cache_read(cache, table, lens, "20"), lambda: kq.cache_read(cache, table, lens, 20, k=k, v=k),
                 lambda: kq.KVCache(cache.k_codes, cache.k_scales, cache.v_codes[:2], cache.v_scales, 64),
                 lambda: kq.KVCache(cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales, 96),
                 lambda: kq.cache_alloc(4, 24, 2, 64, device=DEV)):

@@ -491,7 +491,7 @@ AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_le
   // less than decoding the cache to memory: 8 x 8 heads of 128 over 16384
   // positions, 64 rows 235 against 295 us, 96 rows 328 against 301.  Past 4 GiB of
   // decoded tiles it serves any number of rows.
-  p.tensor_core = rows > 64 && images <= (int64_t(1) << 32);
+  p.tensor_core = rows > 64 && images <= (int64_t(1) << 32) && kv_heads < 32768;
   if (p.tensor_core) {
     // Two query tiles a CTA halve what a wide head's keys and values cost in
     // bandwidth; narrow heads fit two CTAs of one tile on an SM, which hide each
@@ -528,6 +528,7 @@ AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_le
 
 template <int kW, int kNT>
 int launch_split(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
+  if (p.n_chunks * p.row_groups >= (int64_t(1) << 31)) return KQ_ERR_INVALID;
   constexpr int smem = split_smem<kW, kNT>();
   const int rc = allow_smem<attn_split_kernel<kW, kNT>>(smem, dev);
   if (rc != KQ_OK) return rc;
@@ -557,7 +558,7 @@ int64_t attention_rows(int64_t batch, int64_t M, int64_t heads, int64_t kv_heads
                        int64_t max_len) {
   if (batch < 1 || batch > 65535 || M < 1 || heads < 1 || kv_heads < 1 || kv_heads > 65535 ||
       heads % kv_heads != 0 || head_dim < 8 || head_dim > 128 || head_dim % 8 != 0 || max_len < 1 ||
-      max_len >= (int64_t(1) << 31) - 65536)
+      max_len > (int64_t(1) << 30))
     return 0;
   if (M > (int64_t(1) << 30) || heads > (int64_t(1) << 30)) return 0;
   const int64_t rows = M * (heads / kv_heads);

@@ -725,7 +725,6 @@ int launch_tc_qt(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, c
 }  // namespace
 
 int launch_attention_tc(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
-  if (2 * a.view.heads > 65535) return KQ_ERR_INVALID;
   const cudaError_t e = launch_pdl(
       attn_decode_kernel,
       dim3(static_cast<unsigned>(p.tiles), static_cast<unsigned>(2 * a.view.heads), static_cast<unsigned>(batch)),

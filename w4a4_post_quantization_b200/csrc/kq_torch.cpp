@@ -255,6 +255,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (x[i].sizes() != at::IntArrayRef(shape)) refuse(std::string(name) + " must be [batch, tokens, heads, head_dim]");
       disjoint(x[i], name);
     }
+    if (x[0].numel() > 0 && x[0].data_ptr() == x[1].data_ptr()) refuse("k and v must not share memory");
     if (!call("kq_cache_read", c.dev, [&](void* st) {
           return g.cache_read(c.c, static_cast<int32_t*>(table.data_ptr()), B, table.size(1), T,
                               static_cast<int32_t*>(ptr(start)), static_cast<int32_t*>(ptr(lens)), x[0].data_ptr(),
@@ -281,6 +282,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t max_len = a[7] == Py_None ? room : integer(a[7], "max_len");
     if (max_len < 1 || max_len > room) refuse("max_len must be from 1 to what the block table holds");
     const int causal = PyObject_IsTrue(a[5]);
+    if (causal < 0) return nullptr;
     double scale = 1.0 / std::sqrt(static_cast<double>(D));
     if (a[6] != Py_None) {
       scale = PyFloat_AsDouble(a[6]);

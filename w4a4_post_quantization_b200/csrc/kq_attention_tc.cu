@@ -77,19 +77,19 @@ __global__ void __launch_bounds__(kDecodeThreads) attn_decode_kernel(const AttnA
   const int tile = blockIdx.x, hk = blockIdx.y >> 1, tid = threadIdx.x;
   const bool is_v = blockIdx.y & 1;
   const int64_t b = blockIdx.z;
+  const int pos0 = tile * kKv, nb = a.view.nb;
+  // The table's entries beside the length, not after it.
+  const int64_t row = tid < kKv / 16 ? cache_row(a.view, b, pos0 + 16 * tid, hk) : -1;
   const int len = seq_len(a, b);
-  const int pos0 = tile * kKv;
   if (pos0 >= len) return;
-  const int nb = a.view.nb;
   __shared__ int64_t rows[kKv / 16];           // cache row of each 16 positions, -1: none
   __shared__ uint32_t there[kKv / 32];         // which positions there are
   __shared__ __align__(16) uint8_t codes[kKv * 64];
   __shared__ __align__(16) uint8_t scales[kKv * 4];
   if (tid < kKv / 16) {
-    const int pos = pos0 + 16 * tid;
-    const int64_t r = pos < len ? cache_row(a.view, b, pos, hk) : -1;
-    rows[tid] = r;
-    if (r < 0 && pos < len) atomicOr(a.err, kErrCacheIndex);
+    const bool in = pos0 + 16 * tid < len;
+    rows[tid] = in ? row : -1;
+    if (in && row < 0) atomicOr(a.err, kErrCacheIndex);
   }
   __syncthreads();
   if (tid < kKv / 32) {
@@ -529,62 +529,58 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
       auto words_u = [&](int j) { return min(4, (span - j * kKv + 31) >> 5); };
       auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_spin(bar, parity); };
       if (elect_one()) {
-      constexpr uint32_t id_o = idesc_bf16(d16);
-      const uint32_t aq = smem_addr(sq) + t * img, ak = smem_addr(sk), av = smem_addr(sv);
-      const uint32_t ts = tm + t * kKv, to = tm + kQT * kKv + t * 128;
-      // S of tile j, in K stage s; with it that stage has been read.
-      auto scores = [&](int s, int j) {
-        const uint32_t kk = ak + s * img;
-        const uint32_t id = idesc_bf16(0) | static_cast<uint32_t>(words_u(j)) << 19;    // N = 32 words
-        {
+        constexpr uint32_t id_o = idesc_bf16(d16);
+        const uint32_t aq = smem_addr(sq) + t * img, ak = smem_addr(sk), av = smem_addr(sv);
+        const uint32_t ts = tm + t * kKv, to = tm + kQT * kKv + t * 128;
+        // S of tile j, in K stage s; with it that stage has been read.
+        auto scores = [&](int s, int j) {
+          const uint32_t kk = ak + s * img;
+          const uint32_t id = idesc_bf16(0) | static_cast<uint32_t>(words_u(j)) << 19;    // N = 32 words
 #pragma unroll
           for (int k = 0; k < d16 / 16; ++k)
             mma_ss(ts, panel_desc<kD16>(aq, k), panel_desc<kD16>(kk, k), id, k != 0);
           mma_commit(&s_full[t]);
           mma_commit(&k_empty[s]);
-        }
-      };
-      // K steps (16 positions) first .. first + 3 of the second product.
-      auto output = [&](int s, int first, int n_k, bool fresh) {
-        const uint64_t v = smem_desc_sw128(av + s * img) + first * (d16 * 32) / 16;
-        if (n_k >= 4) {
-          {
+        };
+        // K steps (16 positions) first .. first + 3 of the second product.
+        auto output = [&](int s, int first, int n_k, bool fresh) {
+          const uint64_t v = smem_desc_sw128(av + s * img) + first * (d16 * 32) / 16;
+          if (n_k >= 4) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               mma_ts(to, ts + 8 * (first + k), v + 2 * k, id_o, k != 0 || !fresh);
+          } else if (n_k > 0) {
+            for (int k = 0; k < n_k; ++k)
+              mma_ts(to, ts + 8 * (first + k), v + 2 * k, id_o, k != 0 || !fresh);
           }
-        } else if (n_k > 0) {
-          for (int k = 0; k < n_k; ++k)
-            mma_ts(to, ts + 8 * (first + k), v + 2 * k, id_o, k != 0 || !fresh);
+        };
+        bool ok = wait(&q_full[t], 0) && wait(&k_full[0], 0);
+        tmem_fence_after();
+        if (ok) scores(0, 0);
+        for (int j = 0; j < n_u && ok; ++j) {
+          const int s = j % kStages, sn = (j + 1) % kStages;
+          const int steps = 2 * words_u(j);
+          // The loads first: they are there long before the weights.  With one
+          // stage the next K follows the end of these scores' products.
+          ok = wait(&v_full[s], (j / kStages) & 1);
+          if (j + 1 < n_u) ok = ok && wait(&k_full[sn], ((j + 1) / kStages) & 1);
+          ok = ok && wait(&p_half[2 * t], j & 1);
+          if (!ok) break;
+          tmem_fence_after();
+          output(s, 0, min(steps, 4), j == 0);
+          if (!(ok = wait(&p_half[2 * t + 1], j & 1))) break;
+          tmem_fence_after();
+          output(s, 4, steps - 4, false);
+          mma_commit(&v_empty[s]);
+          // The next scores take the place of these weights: MMAs of one thread
+          // run in the order of their issue.
+          if (j + 1 < n_u) scores(sn, j + 1);
         }
-      };
-      bool ok = wait(&q_full[t], 0) && wait(&k_full[0], 0);
-      tmem_fence_after();
-      if (ok) scores(0, 0);
-      for (int j = 0; j < n_u && ok; ++j) {
-        const int s = j % kStages, sn = (j + 1) % kStages;
-        const int steps = 2 * words_u(j);
-        // The loads first: they are there long before the weights.  With one
-        // stage the next K follows the end of these scores' products.
-        ok = wait(&v_full[s], (j / kStages) & 1);
-        if (j + 1 < n_u) ok = ok && wait(&k_full[sn], ((j + 1) / kStages) & 1);
-        ok = ok && wait(&p_half[2 * t], j & 1);
-        if (!ok) break;
-        tmem_fence_after();
-        output(s, 0, min(steps, 4), j == 0);
-        if (!(ok = wait(&p_half[2 * t + 1], j & 1))) break;
-        tmem_fence_after();
-        output(s, 4, steps - 4, false);
-        mma_commit(&v_empty[s]);
-        // The next scores take the place of these weights: MMAs of one thread
-        // run in the order of their issue.
-        if (j + 1 < n_u) scores(sn, j + 1);
-      }
-      if (!ok) atomicOr(a.err, kErrConsumerWait);
-      // Every MMA has completed before the epilogue, and before the columns
-      // are released.
-      mma_commit(&o_full[t]);
-      mbar_wait(&o_full[t], 0);
+        if (!ok) atomicOr(a.err, kErrConsumerWait);
+        // Every MMA has completed before the epilogue, and before the columns
+        // are released.
+        mma_commit(&o_full[t]);
+        mbar_wait(&o_full[t], 0);
       }
     }
     __syncwarp();

@@ -508,10 +508,10 @@ AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_le
     p.nt = rows > 16 ? 4 : rows > 8 ? 2 : 1;
     p.row_groups = static_cast<int>((rows + 8 * p.nt - 1) / (8 * p.nt));
     constexpr int64_t kStep = kTile * kWarps;
-    // About eight CTAs for each SM, of at least 512 positions (8 x 8 heads,
-    // 18 to 33 thousand positions: four 96 us, eight 93, sixteen 100).
+    // About twelve CTAs for each SM, of at least 512 positions (8 x 8 heads, 18 to
+    // 33 thousand positions: six 96 us, eight 87, twelve 85, twenty-four 90).
     const int64_t units = batch * kv_heads * p.row_groups;
-    const int64_t want = std::max<int64_t>(1, 8 * kSms / units);
+    const int64_t want = std::max<int64_t>(1, 12 * kSms / units);
     const int64_t chunk = std::max<int64_t>(512, (max_len + want - 1) / want);
     p.chunk = (chunk + kStep - 1) / kStep * kStep;
   }

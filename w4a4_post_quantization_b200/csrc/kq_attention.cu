@@ -92,10 +92,19 @@ __global__ void __launch_bounds__(32 * kWarps, kNT == 1 ? 4 : kNT == 2 ? 3 : 2)
   const int64_t b = blockIdx.z;
   pdl_wait_then_trigger();
 
+  const int begin = chunk * a.chunk;
+  // This warp's tile i: positions begin + 32 (warp + 4 i).
+  auto tile_pos = [&](int i) { return begin + kTile * (warp + kWarps * i); };
+  // The table's entry for half (lane mod 2) of tile i + lane / 2.
+  auto table_entry = [&](int i) {
+    const int at = (tile_pos(i + (lane >> 1)) + 16 * (lane & 1)) >> a.view.page_shift;
+    return at < a.view.table_pages ? __ldg(a.view.table + b * a.view.table_pages + at) : -1;
+  };
+  // The first 16 tiles' beside the length, not after it.
+  int entry = table_entry(0);
   const int len = seq_len(a, b);
   const int first_limit = row_limit(a, len, r0);                       // the fewest a row sees
   const int last_limit = row_limit(a, len, min(r0 + kRows, a.rows) - 1);
-  const int begin = chunk * a.chunk;
   const int end = min(begin + a.chunk, last_limit);
   int limit[kNT][2];
 #pragma unroll
@@ -104,25 +113,20 @@ __global__ void __launch_bounds__(32 * kWarps, kNT == 1 ? 4 : kNT == 2 ? 3 : 2)
     limit[t][1] = row_limit(a, len, r0 + 8 * t + 2 * c + 1);
   }
 
-  // This warp's tiles: positions begin + 32 (warp + 4 i).
   const int n_tiles = end > begin + kTile * warp
                           ? (end - begin - kTile * warp + kTile * kWarps - 1) / (kTile * kWarps) : 0;
   uint8_t* ring = smem + warp * (kStages * G::kStage);
-  auto tile_pos = [&](int i) { return begin + kTile * (warp + kWarps * i); };
   // Pages of 16 tiles at a time, lane 2 i + half holding half `half` of tile
   // i: the table is read once, ahead of the loads that need it.  -1: nothing
   // to load there.
   int page = -1;
   auto load_pages = [&](int i) {
     const int pos = tile_pos(i + (lane >> 1)) + 16 * (lane & 1);
+    if (i > 0) entry = table_entry(i);
     page = -1;
     if (i + (lane >> 1) < n_tiles && pos < end) {
-      const int at = pos >> a.view.page_shift;
-      if (at < a.view.table_pages) page = __ldg(a.view.table + b * a.view.table_pages + at);
-      if (page < 0 || page >= a.view.pages) {
-        page = -1;
-        atomicOr(a.err, kErrCacheIndex);
-      }
+      if (entry >= 0 && entry < a.view.pages) page = entry;
+      else atomicOr(a.err, kErrCacheIndex);
     }
   };
   uint32_t absent = 0;                        // bit 2 (i mod kStages) + half: that half has no page

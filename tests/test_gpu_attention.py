@@ -186,6 +186,16 @@ def test_wide_value_ranges(M):
     check(out, None, q.double().numpy(), kd, vd, [L], False)
 
 
+@pytest.mark.parametrize("M,Hkv,D,causal", [(140, 2, 64, False), (100, 4, 128, True)])
+@pytest.mark.parametrize("empty", [0, 1, 2, 5])
+def test_many_sequences_with_empty_ones_among_them(M, Hkv, D, causal, empty):
+    """Several times as much work as a GPU holds at once, so that a block takes
+    sequences of every length one after another; ``empty`` of six have none."""
+    B = 130
+    lens = [0 if b % 6 < empty else 1 + (37 * b) % 150 for b in range(B)]
+    run(B, M, Hkv, Hkv, D, 150, 32, lens, causal, seed=empty)
+
+
 @pytest.mark.parametrize("M", [1, 140])
 def test_max_len_bounds_lens(M):
     """Lengths above max_len count as max_len, negative ones as 0."""

@@ -24,6 +24,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "kq_attention.cuh"
 #include "kq_tc.cuh"
 
@@ -233,8 +235,8 @@ struct TcGeom {
   // (its registers go to the others: (kQT kSoftRegs + kRestRegs) is within
   // what (kQT + 1) warpgroups are launched with).
   static constexpr int kThreads = 128 * (kQT + 1);
-  static constexpr int kSoftRegs = kQT == 2 ? 208 : 200;
-  static constexpr int kRestRegs = kQT == 2 ? 80 : 56;
+  static constexpr int kSoftRegs = kQT == 2 ? 208 : 184;
+  static constexpr int kRestRegs = kQT == 2 ? 80 : 72;
   static constexpr int kTmem = 256 * kQT;      // S (128 columns), then O (up to 128), per query tile
   // Q tiles, K and V stages, barriers.
   static constexpr int kSmem = 1024 + (kQT + 2 * kStages) * 256 * kD16 + 256;
@@ -392,9 +394,91 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sc,
   l += s0 + s1;
 }
 
+// An item of work: query tiles of one K/V head of one sequence over one part of the
+// positions.
+struct Item {
+  int64_t b;
+  int hk, chunk, r0;
+  int len, begin, end, n;                      // n: tiles of positions
+};
+
+// Item w: the latest rows first (in a causal call they see most).
+template <int kQT>
+__device__ __forceinline__ Item place_item(const AttnArgs& a, uint32_t w) {
+  Item it;
+  const uint32_t row_tiles = (a.rows + kQT * kQr - 1) / (kQT * kQr);
+  uint32_t q = w / a.n_chunks;
+  it.chunk = static_cast<int>(w - q * a.n_chunks);
+  w = q / row_tiles;
+  it.r0 = static_cast<int>(row_tiles - 1 - (q - w * row_tiles)) * (kQT * kQr);
+  q = w / a.view.heads;
+  it.hk = static_cast<int>(w - q * a.view.heads);
+  it.b = q;
+  it.len = it.begin = it.end = it.n = 0;
+  return it;
+}
+template <int kQT>
+__device__ __forceinline__ Item item_span(const AttnArgs& a, Item it) {
+  it.len = seq_len(a, it.b);
+  it.begin = it.chunk * a.chunk;
+  it.end = min(it.begin + a.chunk, row_limit(a, it.len, min(it.r0 + kQT * kQr, a.rows) - 1));
+  it.n = it.end > it.begin ? (it.end - it.begin + kKv - 1) / kKv : 0;
+  return it;
+}
+
+// The block's next item.  With two query tiles it has one, and saying so here lets the
+// compiler drop what counts over items (2048 x 8192 causal: 239 against 241 us).
+template <int kQT>
+__device__ __forceinline__ uint32_t next_item(uint32_t w, uint32_t items) {
+  return kQT == 1 ? w + gridDim.x : items;
+}
+
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(real ? 16 : 0)
+               : "memory");
+}
+
+// 32 kQuarters rows of queries (from quarter `q` on of the item's tile t) into the
+// swizzled tile at `tile`, by one warp: a row's 16-byte chunks to neighbouring
+// lanes, all copies in flight together (through registers in three groups, the
+// two warps that fetch the next item's queries took 10000 cycles, longer than the
+// item).  A negative scale goes into the queries' signs.
+template <int kD16, int kQuarters>
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, uint8_t* tile, int t, int q,
+                                             int lane) {
+  constexpr int kNc = kD16 / 8, kDr = 32 / kNc, kDc = 32 - kDr * kNc;   // a step of 32 chunks
+  const int qr0 = lane / kNc, qc0 = lane - qr0 * kNc;
+  int qr = qr0, qc = qc0;
+  auto step = [&] {
+    qr += kDr;
+    qc += kDc;
+    if (qc >= kNc) qc -= kNc, ++qr;
+  };
+#pragma unroll 2
+  for (int k = 0; k < kQuarters * kNc; ++k, step()) {
+    const int rr = q * 32 + qr, rg = it.r0 + t * kQr + rr;
+    const bool real = rg < a.rows && 8 * qc < a.D;
+    const int mm = real ? a.group.div(rg) : 0, hh = it.hk * a.group.d + (real ? rg - mm * a.group.d : 0);
+    cp_async16_or_zero(tile + panel_chunk(kD16, rr, qc),
+                       a.q + it.b * a.qb + mm * a.qm + hh * a.qh + (real ? 8 * qc : 0), real);
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (a.scale_log2 < 0.0f) {
+    qr = qr0, qc = qc0;
+    for (int k = 0; k < kQuarters * kNc; ++k, step()) {
+      uint4* x = reinterpret_cast<uint4*>(tile + panel_chunk(kD16, q * 32 + qr, qc));
+      const uint4 y = *x;
+      *x = make_uint4(y.x ^ 0x80008000u, y.y ^ 0x80008000u, y.z ^ 0x80008000u, y.w ^ 0x80008000u);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 template <int kQT, int kD16>
 __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
-    attn_tc_kernel(const AttnArgs a) {
+    attn_tc_kernel(const AttnArgs a, uint32_t items) {
   using G = TcGeom<kQT, kD16>;
   constexpr int kStages = G::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -408,19 +492,13 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
   uint64_t* v_full = k_empty + kStages;
   uint64_t* v_empty = v_full + kStages;
   uint64_t* q_full = v_empty + kStages;
-  uint64_t* s_full = q_full + kQT;
+  uint64_t* q_empty = q_full + kQT;
+  uint64_t* s_full = q_empty + 1;
   uint64_t* p_half = s_full + kQT;            // [query tile][half of the weights]
   uint64_t* o_full = p_half + 2 * kQT;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + kQT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kSoft = 4 * kQT;               // softmax warps
-  const int hk = blockIdx.y;
-  const int64_t b = blockIdx.z;
-  // The latest rows first: in a causal call they see most.
-  const int row_tiles = gridDim.x / a.n_chunks;
-  const int chunk = blockIdx.x % a.n_chunks;
-  const int r0 = (row_tiles - 1 - static_cast<int>(blockIdx.x) / a.n_chunks) * (kQT * kQr);
-
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&k_full[s], 1);
@@ -428,6 +506,7 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], kQT);
     }
+    mbar_init(q_empty, 1);
     for (int t = 0; t < kQT; ++t) {
       mbar_init(&q_full[t], 4);
       mbar_init(&o_full[t], 1);
@@ -443,206 +522,215 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
   tmem_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // The first item's queries.  Before the wait for the decoded tiles: whatever wrote
+  // them was complete before the decoding kernel let this one start.
   if (warp < kSoft) {
-    // A softmax warp's 32 rows into the swizzled Q tile, a row's 16-byte chunks to
-    // neighbouring lanes, all loads in flight together; a negative scale goes into
-    // their signs.  Before the wait for the decoded tiles: whatever wrote the
-    // queries was complete before the decoding kernel let this one start.
-    constexpr int kNc = d16 / 8, kDr = 32 / kNc, kDc = 32 - kDr * kNc;   // a step of 32 items
-    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
-    const int t = warp >> 2;
-    int qr = lane / kNc, qc = lane - qr * kNc;
-    uint8_t* tile = sq + t * img;
-    uint4 x[kNc];
-#pragma unroll
-    for (int k = 0; k < kNc; ++k) {
-      const int rg = r0 + t * kQr + (warp & 3) * 32 + qr;
-      x[k] = make_uint4(0, 0, 0, 0);
-      if (rg < a.rows && 8 * qc < a.D) {
-        const int mm = a.group.div(rg), hh = hk * a.group.d + rg - mm * a.group.d;
-        x[k] = __ldg(reinterpret_cast<const uint4*>(a.q + b * a.qb + mm * a.qm + hh * a.qh) + qc);
-      }
-      qr += kDr;
-      qc += kDc;
-      if (qc >= kNc) qc -= kNc, ++qr;
-    }
-    qr = lane / kNc, qc = lane - qr * kNc;
-#pragma unroll
-    for (int k = 0; k < kNc; ++k) {
-      *reinterpret_cast<uint4*>(tile + panel_chunk(d16, (warp & 3) * 32 + qr, qc)) =
-          make_uint4(x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip);
-      qr += kDr;
-      qc += kDc;
-      if (qc >= kNc) qc -= kNc, ++qr;
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&q_full[t]);
+    load_queries<kD16, 1>(a, place_item<kQT>(a, blockIdx.x), sq + (warp >> 2) * img, warp >> 2, warp & 3, lane);
+    if (lane == 0) mbar_arrive(&q_full[warp >> 2]);
   }
   pdl_wait_then_trigger();
-
-  const int len = seq_len(a, b);
-  const int last_limit = row_limit(a, len, min(r0 + kQT * kQr, a.rows) - 1);
-  const int begin = chunk * a.chunk;
-  const int end = min(begin + a.chunk, last_limit);
-  const int n = end > begin ? (end - begin + kKv - 1) / kKv : 0;
-  const int tile0 = begin / kKv;
-  // Words of 32 positions of tile j that any row of the block sees.
-  auto words = [&](int j) { return min(4, (end - begin - j * kKv + 31) >> 5); };
 
   if (warp >= kSoft) {
     regs_down<G::kRestRegs>();
     if (warp == kSoft && lane == 0) {
       // ---------------------------------------------------------- loads
-      const uint8_t* src = a.images + ((b * a.view.heads + hk) * a.tiles + tile0) * (2ll * img);
       bool ok = true;
-      int j = 0;
-      for (; j < n; ++j) {
-        const int s = j % kStages;
-        const uint32_t ph = ((j / kStages) - 1) & 1;
-        if (j >= kStages && !(ok = mbar_wait(&k_empty[s], ph))) break;
-        mbar_arrive_expect_tx(&k_full[s], img);
-        bulk_load_1d(sk + s * img, src + 2ll * img * j, img, &k_full[s]);
-        if (j >= kStages && !(ok = mbar_wait(&v_empty[s], ph))) {
-          mbar_wait(&k_full[s], (j / kStages) & 1);
-          break;
+      uint32_t g = 0;                          // tiles loaded, over all items
+      for (uint32_t w = blockIdx.x; w < items && ok; w = next_item<kQT>(w, items)) {
+        const Item it = item_span<kQT>(a, place_item<kQT>(a, w));
+        const uint8_t* src =
+            a.images + ((it.b * a.view.heads + it.hk) * a.tiles + it.begin / kKv) * (2ll * img);
+        for (int j = 0; j < it.n; ++j, ++g) {
+          const int s = g % kStages;
+          const uint32_t ph = ((g / kStages) - 1) & 1;
+          if (g >= kStages && !(ok = mbar_wait(&k_empty[s], ph))) break;
+          mbar_arrive_expect_tx(&k_full[s], img);
+          bulk_load_1d(sk + s * img, src + 2ll * img * j, img, &k_full[s]);
+          if (g >= kStages && !(ok = mbar_wait(&v_empty[s], ph))) {
+            mbar_wait(&k_full[s], (g / kStages) & 1);
+            break;
+          }
+          mbar_arrive_expect_tx(&v_full[s], img);
+          bulk_load_1d(sv + s * img, src + 2ll * img * j + img, img, &v_full[s]);
         }
-        mbar_arrive_expect_tx(&v_full[s], img);
-        bulk_load_1d(sv + s * img, src + 2ll * img * j + img, img, &v_full[s]);
       }
       if (!ok) {
         // The copies in flight land before the block ends.
         atomicOr(a.err, kErrProducerWait);
-        for (int i = j > kStages ? j - kStages : 0; i < j; ++i) {
+        for (uint32_t i = g > kStages ? g - kStages : 0; i < g; ++i) {
           mbar_wait(&k_full[i % kStages], (i / kStages) & 1);
           mbar_wait(&v_full[i % kStages], (i / kStages) & 1);
         }
       }
     }
-    if (warp > kSoft && warp <= kSoft + kQT && n > 0) {
+    if constexpr (kQT == 1) {
+      if (warp >= kSoft + 2) {
+        // ----------------------- the next items' queries, half a tile a warp
+        // (each warp stands for two of the softmax warps' four arrivals).
+        uint32_t i = 1;
+        for (uint32_t w = blockIdx.x + gridDim.x; w < items; w += gridDim.x, ++i) {
+          if (!__all_sync(0xFFFFFFFFu, mbar_wait(q_empty, (i - 1) & 1))) {
+            if (lane == 0) atomicOr(a.err, kErrProducerWait);
+            break;
+          }
+          const Item it = place_item<kQT>(a, w);
+          load_queries<kD16, 2>(a, it, sq, 0, 2 * (warp - kSoft - 2), lane);
+          if (lane == 0) {
+            mbar_arrive(&q_full[0]);
+            mbar_arrive(&q_full[0]);
+          }
+        }
+      }
+    }
+    if (warp > kSoft && warp <= kSoft + kQT) {
       // ------------------------------------- MMAs, a warp per query tile
       // Warp reductions and votes hand their results over in uniform registers.
       constexpr uint32_t kAll = 0xFFFFFFFFu;
       const uint32_t tm = __reduce_max_sync(kAll, tmem);
-      const int n_u = __reduce_max_sync(kAll, n), span = __reduce_max_sync(kAll, end - begin);
       const int t = __reduce_max_sync(kAll, warp) - kSoft - 1;
-      auto words_u = [&](int j) { return min(4, (span - j * kKv + 31) >> 5); };
-      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_spin(bar, parity); };
-      if (elect_one()) {
-        constexpr uint32_t id_o = idesc_bf16(d16);
-        const uint32_t aq = smem_addr(sq) + t * img, ak = smem_addr(sk), av = smem_addr(sv);
-        const uint32_t ts = tm + t * kKv, to = tm + kQT * kKv + t * 128;
-        // S of tile j, in K stage s; with it that stage has been read.
-        auto scores = [&](int s, int j) {
-          const uint32_t kk = ak + s * img;
-          const uint32_t id = idesc_bf16(0) | static_cast<uint32_t>(words_u(j)) << 19;    // N = 32 words
+      constexpr uint32_t id_o = idesc_bf16(d16);
+      const uint32_t aq = smem_addr(sq) + t * img, ak = smem_addr(sk), av = smem_addr(sv);
+      const uint32_t ts = tm + t * kKv, to = tm + kQT * kKv + t * 128;
+      bool ok = true;
+      uint32_t g0 = 0, i = 0, done = 0;        // tiles, items, items with tiles so far
+      for (uint32_t w = blockIdx.x; w < items && ok; w = next_item<kQT>(w, items), ++i) {
+        const Item it = item_span<kQT>(a, place_item<kQT>(a, w));
+        const int n = __reduce_max_sync(kAll, it.n), span = __reduce_max_sync(kAll, it.end - it.begin);
+        auto words = [&](int j) { return min(4, (span - j * kKv + 31) >> 5); };
+        if (elect_one()) {
+          // S of tile j; with it its K stage has been read, and with the last one
+          // the queries.
+          auto scores = [&](int j) {
+            const int s = (g0 + j) % kStages;
+            const uint32_t kk = ak + s * img;
+            const uint32_t id = idesc_bf16(0) | static_cast<uint32_t>(words(j)) << 19;    // N = 32 words
 #pragma unroll
-          for (int k = 0; k < d16 / 16; ++k)
-            mma_ss(ts, panel_desc<kD16>(aq, k), panel_desc<kD16>(kk, k), id, k != 0);
-          mma_commit(&s_full[t]);
-          mma_commit(&k_empty[s]);
-        };
-        // K steps (16 positions) first .. first + 3 of the second product.
-        auto output = [&](int s, int first, int n_k, bool fresh) {
-          const uint64_t v = smem_desc_sw128(av + s * img) + first * (d16 * 32) / 16;
-          if (n_k >= 4) {
+            for (int k = 0; k < d16 / 16; ++k)
+              mma_ss(ts, panel_desc<kD16>(aq, k), panel_desc<kD16>(kk, k), id, k != 0);
+            mma_commit(&s_full[t]);
+            mma_commit(&k_empty[s]);
+            if (kQT == 1 && j + 1 == n) mma_commit(q_empty);
+          };
+          // K steps (16 positions) first .. first + 3 of the second product.
+          auto output = [&](int s, int first, int n_k, bool fresh) {
+            const uint64_t v = smem_desc_sw128(av + s * img) + first * (d16 * 32) / 16;
+            if (n_k >= 4) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_ts(to, ts + 8 * (first + k), v + 2 * k, id_o, k != 0 || !fresh);
-          } else if (n_k > 0) {
-            for (int k = 0; k < n_k; ++k)
-              mma_ts(to, ts + 8 * (first + k), v + 2 * k, id_o, k != 0 || !fresh);
+              for (int k = 0; k < 4; ++k)
+                mma_ts(to, ts + 8 * (first + k), v + 2 * k, id_o, k != 0 || !fresh);
+            } else if (n_k > 0) {
+              for (int k = 0; k < n_k; ++k)
+                mma_ts(to, ts + 8 * (first + k), v + 2 * k, id_o, k != 0 || !fresh);
+            }
+          };
+          // The last item's weights have been multiplied in their order before
+          // these scores take their place; its O is read by the warps that then
+          // make this one's first weights.
+          ok = mbar_spin(&q_full[t], i & 1);
+          if (n == 0) {
+            if (kQT == 1) mbar_arrive(q_empty);
+          } else {
+            ok = ok && mbar_spin(&k_full[g0 % kStages], (g0 / kStages) & 1);
+            tmem_fence_after();
+            if (ok) scores(0);
           }
-        };
-        bool ok = wait(&q_full[t], 0) && wait(&k_full[0], 0);
-        tmem_fence_after();
-        if (ok) scores(0, 0);
-        for (int j = 0; j < n_u && ok; ++j) {
-          const int s = j % kStages, sn = (j + 1) % kStages;
-          const int steps = 2 * words_u(j);
-          // The loads first: they are there long before the weights.  With one
-          // stage the next K follows the end of these scores' products.
-          ok = wait(&v_full[s], (j / kStages) & 1);
-          if (j + 1 < n_u) ok = ok && wait(&k_full[sn], ((j + 1) / kStages) & 1);
-          ok = ok && wait(&p_half[2 * t], j & 1);
-          if (!ok) break;
-          tmem_fence_after();
-          output(s, 0, min(steps, 4), j == 0);
-          if (!(ok = wait(&p_half[2 * t + 1], j & 1))) break;
-          tmem_fence_after();
-          output(s, 4, steps - 4, false);
-          mma_commit(&v_empty[s]);
-          // The next scores take the place of these weights: MMAs of one thread
-          // run in the order of their issue.
-          if (j + 1 < n_u) scores(sn, j + 1);
+          for (int j = 0; j < n && ok; ++j) {
+            const uint32_t g = g0 + j, s = g % kStages;
+            const int steps = 2 * words(j);
+            // The loads first: they are there long before the weights.  With one
+            // stage the next K follows the end of these scores' products.
+            ok = mbar_spin(&v_full[s], (g / kStages) & 1);
+            if (j + 1 < n) ok = ok && mbar_spin(&k_full[(g + 1) % kStages], ((g + 1) / kStages) & 1);
+            ok = ok && mbar_spin(&p_half[2 * t], g & 1);
+            if (!ok) break;
+            tmem_fence_after();
+            output(s, 0, min(steps, 4), j == 0);
+            if (!(ok = mbar_spin(&p_half[2 * t + 1], g & 1))) break;
+            tmem_fence_after();
+            output(s, 4, steps - 4, false);
+            mma_commit(&v_empty[s]);
+            // The next scores take the place of these weights: MMAs of one thread
+            // run in the order of their issue.
+            if (j + 1 < n) scores(j + 1);
+          }
+          if (!ok) atomicOr(a.err, kErrConsumerWait);
+          // Every MMA of the item has completed before its epilogue.  (An item without
+          // tiles has no MMA to wait for, and its softmax warps do not: with a phase
+          // of its own, this thread could be two ahead of them.)
+          if (n > 0) mma_commit(&o_full[t]);
         }
-        if (!ok) atomicOr(a.err, kErrConsumerWait);
-        // Every MMA has completed before the epilogue, and before the columns
-        // are released.
-        mma_commit(&o_full[t]);
-        mbar_wait(&o_full[t], 0);
+        ok = __all_sync(kAll, ok);
+        g0 += n;
+        done += n > 0;
       }
+      // And before the columns are released.
+      if (done > 0) mbar_wait(&o_full[t], (done - 1) & 1);
     }
     __syncwarp();
   } else {
     // ----------------------------------------------------------- softmax
     regs_up<G::kSoftRegs>();
     const int t = warp >> 2, row = (warp & 3) * 32 + lane;
-    const int r = r0 + t * kQr + row;
-    const bool mine = r < a.rows;
-    const int m = mine ? a.group.div(r) : 0, h = hk * a.group.d + (mine ? r - m * a.group.d : 0);
     // Not zero: a masked score, -inf, stays -inf through it.
     const float sc = fmaxf(fabsf(a.scale_log2) * kUnscale, 1e-38f);
-    const int limit = row_limit(a, len, r);
-    const int tile_limit = row_limit(a, len, min(r0 + t * kQr, a.rows - 1));   // the fewest of the tile
     const uint32_t ts = tmem + (uint32_t((warp & 3) * 32) << 16) + t * kKv;
     const uint32_t to = tmem + (uint32_t((warp & 3) * 32) << 16) + kQT * kKv + t * 128;
-    float mx = -INFINITY, l = 0.0f;
     bool ok = true;
-    if (t == 1 && n > 0) next_turn<kQT>(warp);             // the first turn is tile 0's
-    for (int j = 0; j < n; ++j) {
+    uint32_t g = 0, done = 0;                  // tiles, and items with tiles, so far
+    // The first turn is tile 0's.
+    if (t == 1 && item_span<kQT>(a, place_item<kQT>(a, blockIdx.x)).n > 0) next_turn<kQT>(warp);
+    for (uint32_t w = blockIdx.x; w < items; w = next_item<kQT>(w, items)) {
+      const Item it = item_span<kQT>(a, place_item<kQT>(a, w));
+      const int r = it.r0 + t * kQr + row;
+      const bool mine = r < a.rows;
+      const int m = mine ? a.group.div(r) : 0, h = it.hk * a.group.d + (mine ? r - m * a.group.d : 0);
+      const int limit = row_limit(a, it.len, r);
+      const int tile_limit = row_limit(a, it.len, min(it.r0 + t * kQr, a.rows - 1));   // the fewest of the tile
+      float mx = -INFINITY, l = 0.0f;
+      const uint4* mask = a.tile_mask + it.b * a.tiles + it.begin / kKv;
+      const int n = it.n;
+      int j = 0;
+      for (; j < n && ok; ++j, ++g) {
+        const uint4 there = __ldg(mask + j);
+        ok = __all_sync(0xFFFFFFFFu, mbar_spin(&s_full[t], g & 1));
+        if (!ok) break;
+        tmem_fence_after();
+        const int pos0 = it.begin + j * kKv;
+        const int words = min(4, (it.end - pos0 + 31) >> 5);   // that any row of the block sees
+        uint32_t see[4] = {there.x, there.y, there.z, there.w};
+        if (pos0 + kKv > tile_limit || (there.x & there.y & there.z & there.w) != 0xFFFFFFFFu) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int left = limit - pos0 - 32 * v;          // positions of this word the row sees
+            see[v] = left >= 32 ? see[v] : left <= 0 ? 0u : see[v] & ((1u << left) - 1u);
+          }
+          softmax_tile<false, kD16, kQT>(ts, to, sc, mx, l, j == 0, see, words, p_half + 2 * t, warp, lane,
+                                          t == 1 && j + 1 == n);
+        } else {
+          softmax_tile<true, kD16, kQT>(ts, to, sc, mx, l, j == 0, see, 4, p_half + 2 * t, warp, lane,
+                                          t == 1 && j + 1 == n);
+        }
+      }
       if (!ok) {
         // Gave up: the other tile's turns go on.
-        my_turn<kQT>(warp);
-        if (t == 0 || j + 1 < n) next_turn<kQT>(warp);
-        continue;
-      }
-      const uint4 there = __ldg(a.tile_mask + b * a.tiles + tile0 + j);
-      ok = __all_sync(0xFFFFFFFFu, mbar_spin(&s_full[t], j & 1));
-      if (!ok) {
-        --j;
-        continue;
-      }
-      tmem_fence_after();
-      const int pos0 = begin + j * kKv;
-      uint32_t see[4] = {there.x, there.y, there.z, there.w};
-      if (pos0 + kKv > tile_limit || (there.x & there.y & there.z & there.w) != 0xFFFFFFFFu) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int left = limit - pos0 - 32 * v;          // positions of this word the row sees
-          see[v] = left >= 32 ? see[v] : left <= 0 ? 0u : see[v] & ((1u << left) - 1u);
+        for (; j < n; ++j) {
+          my_turn<kQT>(warp);
+          if (t == 0 || j + 1 < n) next_turn<kQT>(warp);
         }
-        softmax_tile<false, kD16, kQT>(ts, to, sc, mx, l, j == 0, see, words(j), p_half + 2 * t, warp, lane,
-                                        t == 1 && j + 1 == n);
-      } else {
-        softmax_tile<true, kD16, kQT>(ts, to, sc, mx, l, j == 0, see, 4, p_half + 2 * t, warp, lane,
-                                        t == 1 && j + 1 == n);
+        continue;
       }
-    }
-    if (ok && n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[t], 0));
-    if (!ok) {
-      if (lane == 0) atomicOr(a.err, kErrConsumerWait);
-    } else {
+      if (n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[t], done & 1));
+      done += n > 0;
+      if (!ok) continue;
       tmem_fence_after();
       const bool part = a.n_chunks > 1;
-      const int64_t at = ((b * a.view.heads + hk) * a.n_chunks + chunk) * a.rows + r;
+      const int64_t at = ((it.b * a.view.heads + it.hk) * a.n_chunks + it.chunk) * a.rows + r;
       const float inv = l > 0.0f ? kUnscale / l : 0.0f;
-      uint16_t* out = a.out + b * a.ob + m * a.om + h * a.oh;
       float* po = a.part_o + at * (32 * a.view.nb);
-      // 32 channels at a time.  (Unrolled with two query tiles, the loop above
-      // spilled more: 265 against 234 us for 2048 x 8192 causal.)
-      constexpr int kUnroll = kQT == 1 ? 4 : 1;
-#pragma unroll kUnroll
+      uint16_t* out = a.out + it.b * a.ob + m * a.om + h * a.oh;
+      // 32 channels at a time.  (Through shared memory, four lanes to a row's 64 bytes:
+      // 38.8 against 37.5 us for 4096 x 300, 2 x 16 heads of 72.)
+#pragma unroll 1
       for (int c = 0; c < d16; c += 32) {
         uint32_t o[2][16];
 #pragma unroll
@@ -654,33 +742,37 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
           if (c + 16 < d16) tmem_ld16(to + c + 16, o[1]);
           tmem_wait_ld();
         }
-        if (!mine || (part && mx == -INFINITY)) continue;
+        if (mine && part && mx != -INFINITY) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if (c + 16 * u >= d16) continue;
-          if (part) {
+          for (int u = 0; u < 2; ++u)
+            if (c + 16 * u < d16)
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<uint4*>(po + c + 16 * u + e) =
-                  make_uint4(o[u][e], o[u][e + 1], o[u][e + 2], o[u][e + 3]);
-            continue;
-          }
-#pragma unroll
-          for (int e = 0; e < 16; e += 8) {
-            if (c + 16 * u + e >= a.D) continue;
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = bf16x2(__uint_as_float(o[u][e + 2 * k]) * inv, __uint_as_float(o[u][e + 2 * k + 1]) * inv);
-            *reinterpret_cast<uint4*>(out + c + 16 * u + e) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<uint4*>(po + c + 16 * u + e) =
+                    make_uint4(o[u][e], o[u][e + 1], o[u][e + 2], o[u][e + 3]);
         }
+        if (mine && !part) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (c + 8 * x < a.D) {
+              uint32_t w4[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                w4[k] = bf16x2(__uint_as_float(o[x >> 1][8 * (x & 1) + 2 * k]) * inv,
+                               __uint_as_float(o[x >> 1][8 * (x & 1) + 2 * k + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + c + 8 * x) = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            }
+        }
+        __syncwarp();
       }
       if (mine && part) a.part_ml[at] = make_float2(mx, l);
       if (mine && !part && a.lse)
-        a.lse[(b * a.view.heads * a.group.d + h) * a.M + m] =
+        a.lse[(it.b * a.view.heads * a.group.d + h) * a.M + m] =
             mx == -INFINITY ? -INFINITY : (mx + (log2f(l) - kShift)) * kLn2;
+      // O has been read: the next item's first weights come after.
+      tmem_fence_before();
     }
+    if (!ok && lane == 0) atomicOr(a.err, kErrConsumerWait);
     tmem_fence_before();
   }
   __syncthreads();
@@ -705,11 +797,14 @@ int launch_tc(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cuda
   const int rc = allow_smem<attn_tc_kernel<kQT, kD16>>(G::kSmem, dev);
   if (rc != KQ_OK) return rc;
   if (!registers_suffice<kQT, kD16>()) return record_cuda_error(cudaErrorLaunchOutOfResources);
-  const int64_t row_tiles = (a.rows + kQT * kQr - 1) / (kQT * kQr);
-  if (row_tiles * p.n_chunks >= (int64_t(1) << 31)) return KQ_ERR_INVALID;
-  const dim3 grid(static_cast<unsigned>(row_tiles * p.n_chunks), static_cast<unsigned>(a.view.heads),
-                  static_cast<unsigned>(batch));
-  const cudaError_t e = launch_pdl(attn_tc_kernel<kQT, kD16>, grid, dim3(G::kThreads), G::kSmem, st, a);
+  const int64_t items = (a.rows + kQT * kQr - 1) / (kQT * kQr) * p.n_chunks * a.view.heads * batch;
+  if (items > (int64_t(1) << 31) - 65536) return KQ_ERR_INVALID;
+  // One query tile: the blocks that are resident at once take the items in turn,
+  // the next one's queries and keys on their way under the last one's output.
+  const int64_t grid = kQT == 1 ? std::min<int64_t>(items, 2 * 148) : items;
+  const cudaError_t e = launch_pdl(attn_tc_kernel<kQT, kD16>, dim3(static_cast<unsigned>(grid)),
+                                   dim3(G::kThreads), G::kSmem, st, a,
+                                   static_cast<uint32_t>(items));
   return e == cudaSuccess ? KQ_OK : record_cuda_error(e);
 }
 

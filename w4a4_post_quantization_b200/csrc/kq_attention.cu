@@ -497,14 +497,10 @@ AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_le
   // decoded tiles it serves any number of rows.
   p.tensor_core = rows > 64 && images <= (int64_t(1) << 32) && kv_heads < 32768;
   if (p.tensor_core) {
-    // Two query tiles a CTA halve what a wide head's keys and values cost in
-    // bandwidth; narrow heads fit two CTAs of one tile on an SM, which hide each
-    // other's start and end (4096 x 300, 2 x 16 heads of 72: 38 against 45 us).
-    p.q_tiles = d16 <= 80 || rows <= 128 ? 1 : 2;
-    const int64_t units = batch * kv_heads * ((rows + 128 * p.q_tiles - 1) / (128 * p.q_tiles));
-    // Cut along the positions where there are too few CTAs, into parts of at
+    // Cut along the positions where there are too few tiles of rows, into parts of at
     // least four tiles.
-    const int64_t want = std::max<int64_t>(1, std::min(kSms * (p.q_tiles == 2 ? 1 : 2) / units, (p.tiles + 3) / 4));
+    const int64_t units = batch * kv_heads * ((rows + 127) / 128);
+    const int64_t want = std::max<int64_t>(1, std::min(2 * kSms / units, (p.tiles + 3) / 4));
     p.chunk = (p.tiles + want - 1) / want * 128;
     p.mask_bytes = static_cast<size_t>((batch * p.tiles * 16 + 255) / 256 * 256);
     p.image_bytes = static_cast<size_t>(images);

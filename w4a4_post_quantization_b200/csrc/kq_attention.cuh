@@ -98,7 +98,6 @@ constexpr float kUnscale = 4611686018427387904.0f;      // 2^kShift
 struct AttnPlan {
   bool tensor_core;
   int row_groups, nt;              // few rows: groups of 8 nt rows
-  int q_tiles;                     // tensor cores: 128-row tiles of a CTA
   int64_t chunk, n_chunks, tiles;
   size_t ml_bytes, part_bytes, mask_bytes, image_bytes, bytes;
 };

@@ -12,15 +12,21 @@
 // 256 D bytes.  (Panels of 16 throughout, with the 32-byte swizzle, made the
 // operand reads the bound: 2048 x 8192 causal, 32 heads of 128, took 295 us.)
 //
-// The second kernel gives a CTA kQT tiles of 128 rows (query, head of the group)
-// of one K/V head.  Warps 0 .. 4 kQT - 1 hold one row a thread: scores out of
-// tensor memory, the running maximum and sum, weights back into it as bf16 in
-// the scores' place, where the second product reads them.  One thread loads and
-// one issues the MMAs; with two query tiles the products of one run under the
-// softmax of the other (a warp issues for each).  The accumulator O stays in tensor memory.  It is
-// rescaled only when a row's maximum has grown by more than 2^8: until then the
-// weights are relative to the older maximum, which float32 and bf16 hold as
-// well.
+// The second kernel works on items: a tile of 128 rows (query, head of the group) of
+// one K/V head, over all positions or a part of them.  Two blocks are resident on an
+// SM, so that the products of one run under the softmax of the other, and each takes
+// items in turn.  Warps 0 .. 3 hold one row a thread: scores out of tensor memory, the
+// running maximum and sum, weights back into it as bf16 in the scores' place, where
+// the second product reads them.  One thread loads keys and values, one issues the
+// MMAs, and two warps fetch the next item's queries.  The accumulator O stays in
+// tensor memory.  It is rescaled only when a row's maximum has grown by more than 2^8:
+// until then the weights are relative to the older maximum, which float32 and bf16
+// hold as well.  (A block with two query tiles that take turns at the exponentials,
+// alone on its SM, reads keys and values half as often, but nothing covers its start
+// and end: 2048 x 8192 causal, 32 heads of 128, 229 against 232 us, without the mask
+// 240 against 250; 4096 x 4096, 24 heads of 96, 198 against 194; 4096 x 300,
+// 2 x 16 heads, 45 against 38 us for heads of 72, 53 against 45 for 96 and 54
+// against 46 for 128.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -227,20 +233,19 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int n) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(n >> 3) << 17) | (uint32_t(kQr >> 4) << 24);
 }
 
-template <int kQT, int kD16>
+template <int kD16>
 struct TcGeom {
-  // Two blocks of one query tile share an SM: 113 KB each.
-  static constexpr int kStages = kQT == 2 || kD16 <= 80 ? 2 : 1;
-  // Softmax warpgroups, and one whose first two warps load and issue the MMAs
-  // (its registers go to the others: (kQT kSoftRegs + kRestRegs) is within
-  // what (kQT + 1) warpgroups are launched with).
-  static constexpr int kThreads = 128 * (kQT + 1);
-  static constexpr int kSoftRegs = kQT == 2 ? 208 : 184;
-  static constexpr int kRestRegs = kQT == 2 ? 80 : 72;
-  static constexpr int kTmem = 256 * kQT;      // S (128 columns), then O (up to 128), per query tile
-  // Q tiles, K and V stages, barriers.
-  static constexpr int kSmem = 1024 + (kQT + 2 * kStages) * 256 * kD16 + 256;
-  static_assert(kSmem <= (kQT == 2 ? 232448 : 115712), "shared memory");
+  // Two blocks share an SM: 113 KB each.
+  static constexpr int kStages = kD16 <= 80 ? 2 : 1;
+  // A softmax warpgroup, and one that loads and issues the MMAs (its registers go to
+  // the other: the sum of the shares is within what the two are launched with).
+  static constexpr int kThreads = 256;
+  static constexpr int kSoftRegs = 184;
+  static constexpr int kRestRegs = 72;
+  static constexpr int kTmem = 256;            // S (128 columns), then O (up to 128)
+  // Q, K and V stages, barriers.
+  static constexpr int kSmem = 1024 + (1 + 2 * kStages) * 256 * kD16 + 256;
+  static_assert(kSmem <= 115712, "shared memory");
 };
 
 // mbar_wait as one tight loop, for the waits on every tile's critical path; each
@@ -262,24 +267,10 @@ __device__ __forceinline__ bool mbar_spin(uint64_t* bar, uint32_t parity) {
 
 // Every so many pairs of weights of a whole tile take ex2_poly, the others the
 // special-function unit, which alone would need 8 cycles for each of a warp's 128
-// columns.  2048 x 8192 causal, 32 heads of 128: every 2nd 234 us, 3rd 244, 4th
-// 249, none 256; with one query tile a block, which shares the issue slots
-// with another block, 253, 243, 240 and 263.
-template <int kQT>
-constexpr int kPolyEvery = kQT == 2 ? 2 : 4;
-
-// With two query tiles the warps of the two that share a scheduler take turns at
-// the exponentials: while one is at them, the other's products run.  Left alone,
-// both come to wait for their scores at the same time.  Each call of my_turn on one
-// side needs a next_turn on the other; the first turn is tile 0's.
-template <int kQT>
-__device__ __forceinline__ void my_turn(int warp) {
-  if constexpr (kQT == 2) asm volatile("bar.sync %0, 64;" ::"r"(1 + warp) : "memory");
-}
-template <int kQT>
-__device__ __forceinline__ void next_turn(int warp) {
-  if constexpr (kQT == 2) asm volatile("bar.arrive %0, 64;" ::"r"(1 + (warp ^ 4)) : "memory");
-}
+// columns.  2048 x 8192 causal, 32 heads of 128, and 4096 x 300, 2 x 16 heads of 72:
+// every 2nd 265 and 42.0 us, 3rd 248 and 39.2, 4th 234 and 37.8, 5th 237 and 39.0,
+// 6th 231 and 41.0, none 240 and 39.6.
+constexpr int kPolyEvery = 4;
 
 // -inf for the positions a row does not see.
 __device__ __forceinline__ void hide(uint32_t (&x)[32], uint32_t see) {
@@ -300,11 +291,10 @@ __device__ __forceinline__ void weights_ready(uint64_t* bar, int lane) {
 // A row's 128 scores to weights.  kWhole: the row sees every position; else
 // `see` says which, `words` of 32 of them are looked at, and the others' weights
 // are not used.
-template <bool kWhole, int kD16, int kQT>
+template <bool kWhole, int kD16>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sc, float& mx, float& l,
                                              bool first, const uint32_t (&see)[4], int words,
-                                             uint64_t* p_half, int warp, int lane,
-                                             bool last_turn) {
+                                             uint64_t* p_half, int lane) {
   // The maximum of words 2 and 3 is taken first and they are read again later,
   // so that 64 scores at a time are in registers.
   uint32_t x[2][32];
@@ -349,7 +339,6 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sc,
       }
     }
   }
-  my_turn<kQT>(warp);
   const float shift = kShift - (mx == -INFINITY ? 0.0f : mx);
   const f2 sc2 = pack2(sc, sc), shift2 = pack2(shift, shift);
   f2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
@@ -368,7 +357,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sc,
                           shift2);
         float p0, p1;
         unpack2(y, p0, p1);
-        if (kWhole && e % kPolyEvery<kQT> == kPolyEvery<kQT> - 1) {
+        if (kWhole && e % kPolyEvery == kPolyEvery - 1) {
           ex2_poly(pack2(fmaxf(p0, -126.0f), fmaxf(p1, -126.0f)), p0, p1);
         } else {
           p0 = ex2(p0);
@@ -387,14 +376,13 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sc,
     }
     if (v < 2 && (kWhole || v + 2 < words)) tmem_ld32(ts + 32 * (v + 2), x[u]);
   }
-  if (!last_turn) next_turn<kQT>(warp);
   weights_ready(p_half + 1, lane);
   float s0, s1;
   unpack2(add2(sum[0], sum[1]), s0, s1);
   l += s0 + s1;
 }
 
-// An item of work: query tiles of one K/V head of one sequence over one part of the
+// An item of work: a query tile of one K/V head of one sequence over one part of the
 // positions.
 struct Item {
   int64_t b;
@@ -403,34 +391,25 @@ struct Item {
 };
 
 // Item w: the latest rows first (in a causal call they see most).
-template <int kQT>
 __device__ __forceinline__ Item place_item(const AttnArgs& a, uint32_t w) {
   Item it;
-  const uint32_t row_tiles = (a.rows + kQT * kQr - 1) / (kQT * kQr);
+  const uint32_t row_tiles = (a.rows + kQr - 1) / kQr;
   uint32_t q = w / a.n_chunks;
   it.chunk = static_cast<int>(w - q * a.n_chunks);
   w = q / row_tiles;
-  it.r0 = static_cast<int>(row_tiles - 1 - (q - w * row_tiles)) * (kQT * kQr);
+  it.r0 = static_cast<int>(row_tiles - 1 - (q - w * row_tiles)) * kQr;
   q = w / a.view.heads;
   it.hk = static_cast<int>(w - q * a.view.heads);
   it.b = q;
   it.len = it.begin = it.end = it.n = 0;
   return it;
 }
-template <int kQT>
 __device__ __forceinline__ Item item_span(const AttnArgs& a, Item it) {
   it.len = seq_len(a, it.b);
   it.begin = it.chunk * a.chunk;
-  it.end = min(it.begin + a.chunk, row_limit(a, it.len, min(it.r0 + kQT * kQr, a.rows) - 1));
+  it.end = min(it.begin + a.chunk, row_limit(a, it.len, min(it.r0 + kQr, a.rows) - 1));
   it.n = it.end > it.begin ? (it.end - it.begin + kKv - 1) / kKv : 0;
   return it;
-}
-
-// The block's next item.  With two query tiles it has one, and saying so here lets the
-// compiler drop what counts over items (2048 x 8192 causal: 239 against 241 us).
-template <int kQT>
-__device__ __forceinline__ uint32_t next_item(uint32_t w, uint32_t items) {
-  return kQT == 1 ? w + gridDim.x : items;
 }
 
 // 16 bytes from global to shared memory, or zeros.
@@ -439,14 +418,13 @@ __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, b
                : "memory");
 }
 
-// 32 kQuarters rows of queries (from quarter `q` on of the item's tile t) into the
+// 32 kQuarters rows of queries (from quarter `q` on of the item's tile) into the
 // swizzled tile at `tile`, by one warp: a row's 16-byte chunks to neighbouring
 // lanes, all copies in flight together (through registers in three groups, the
 // two warps that fetch the next item's queries took 10000 cycles, longer than the
 // item).  A negative scale goes into the queries' signs.
 template <int kD16, int kQuarters>
-__device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, uint8_t* tile, int t, int q,
-                                             int lane) {
+__device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, uint8_t* tile, int q, int lane) {
   constexpr int kNc = kD16 / 8, kDr = 32 / kNc, kDc = 32 - kDr * kNc;   // a step of 32 chunks
   const int qr0 = lane / kNc, qc0 = lane - qr0 * kNc;
   int qr = qr0, qc = qc0;
@@ -455,9 +433,9 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, 
     qc += kDc;
     if (qc >= kNc) qc -= kNc, ++qr;
   };
-#pragma unroll 2
+#pragma unroll 1
   for (int k = 0; k < kQuarters * kNc; ++k, step()) {
-    const int rr = q * 32 + qr, rg = it.r0 + t * kQr + rr;
+    const int rr = q * 32 + qr, rg = it.r0 + rr;
     const bool real = rg < a.rows && 8 * qc < a.D;
     const int mm = real ? a.group.div(rg) : 0, hh = it.hk * a.group.d + (real ? rg - mm * a.group.d : 0);
     cp_async16_or_zero(tile + panel_chunk(kD16, rr, qc),
@@ -466,6 +444,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, 
   asm volatile("cp.async.wait_all;" ::: "memory");
   if (a.scale_log2 < 0.0f) {
     qr = qr0, qc = qc0;
+#pragma unroll 1
     for (int k = 0; k < kQuarters * kNc; ++k, step()) {
       uint4* x = reinterpret_cast<uint4*>(tile + panel_chunk(kD16, q * 32 + qr, qc));
       const uint4 y = *x;
@@ -476,44 +455,42 @@ __device__ __forceinline__ void load_queries(const AttnArgs& a, const Item& it, 
   __syncwarp();
 }
 
-template <int kQT, int kD16>
-__global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
+template <int kD16>
+__global__ void __launch_bounds__(TcGeom<kD16>::kThreads, 2)
     attn_tc_kernel(const AttnArgs a, uint32_t items) {
-  using G = TcGeom<kQT, kD16>;
+  using G = TcGeom<kD16>;
   constexpr int kStages = G::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   constexpr int d16 = kD16, img = 256 * d16;
   uint8_t* sq = base;
-  uint8_t* sk = sq + kQT * img;
+  uint8_t* sk = sq + img;
   uint8_t* sv = sk + kStages * img;
   uint64_t* k_full = reinterpret_cast<uint64_t*>(sv + kStages * img);
   uint64_t* k_empty = k_full + kStages;
   uint64_t* v_full = k_empty + kStages;
   uint64_t* v_empty = v_full + kStages;
   uint64_t* q_full = v_empty + kStages;
-  uint64_t* q_empty = q_full + kQT;
+  uint64_t* q_empty = q_full + 1;
   uint64_t* s_full = q_empty + 1;
-  uint64_t* p_half = s_full + kQT;            // [query tile][half of the weights]
-  uint64_t* o_full = p_half + 2 * kQT;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + kQT);
+  uint64_t* p_half = s_full + 1;               // for each half of a tile's weights
+  uint64_t* o_full = p_half + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kSoft = 4 * kQT;               // softmax warps
+  constexpr int kSoft = 4;               // softmax warps
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], kQT);
+      mbar_init(&k_empty[s], 1);
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], kQT);
+      mbar_init(&v_empty[s], 1);
     }
+    mbar_init(q_full, 4);
     mbar_init(q_empty, 1);
-    for (int t = 0; t < kQT; ++t) {
-      mbar_init(&q_full[t], 4);
-      mbar_init(&o_full[t], 1);
-      mbar_init(&s_full[t], 1);
-      mbar_init(&p_half[2 * t], 4);
-      mbar_init(&p_half[2 * t + 1], 4);
-    }
+    mbar_init(s_full, 1);
+    mbar_init(&p_half[0], 4);
+    mbar_init(&p_half[1], 4);
+    mbar_init(o_full, 1);
     fence_mbar_init();
   }
   if (warp == kSoft + 1) tmem_alloc(tmem_slot, G::kTmem);
@@ -525,8 +502,8 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
   // The first item's queries.  Before the wait for the decoded tiles: whatever wrote
   // them was complete before the decoding kernel let this one start.
   if (warp < kSoft) {
-    load_queries<kD16, 1>(a, place_item<kQT>(a, blockIdx.x), sq + (warp >> 2) * img, warp >> 2, warp & 3, lane);
-    if (lane == 0) mbar_arrive(&q_full[warp >> 2]);
+    load_queries<kD16, 1>(a, place_item(a, blockIdx.x), sq, warp, lane);
+    if (lane == 0) mbar_arrive(q_full);
   }
   pdl_wait_then_trigger();
 
@@ -536,8 +513,8 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
       // ---------------------------------------------------------- loads
       bool ok = true;
       uint32_t g = 0;                          // tiles loaded, over all items
-      for (uint32_t w = blockIdx.x; w < items && ok; w = next_item<kQT>(w, items)) {
-        const Item it = item_span<kQT>(a, place_item<kQT>(a, w));
+      for (uint32_t w = blockIdx.x; w < items && ok; w += gridDim.x) {
+        const Item it = item_span(a, place_item(a, w));
         const uint8_t* src =
             a.images + ((it.b * a.view.heads + it.hk) * a.tiles + it.begin / kKv) * (2ll * img);
         for (int j = 0; j < it.n; ++j, ++g) {
@@ -563,38 +540,35 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
         }
       }
     }
-    if constexpr (kQT == 1) {
-      if (warp >= kSoft + 2) {
-        // ----------------------- the next items' queries, half a tile a warp
-        // (each warp stands for two of the softmax warps' four arrivals).
-        uint32_t i = 1;
-        for (uint32_t w = blockIdx.x + gridDim.x; w < items; w += gridDim.x, ++i) {
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(q_empty, (i - 1) & 1))) {
-            if (lane == 0) atomicOr(a.err, kErrProducerWait);
-            break;
-          }
-          const Item it = place_item<kQT>(a, w);
-          load_queries<kD16, 2>(a, it, sq, 0, 2 * (warp - kSoft - 2), lane);
-          if (lane == 0) {
-            mbar_arrive(&q_full[0]);
-            mbar_arrive(&q_full[0]);
-          }
+    if (warp >= kSoft + 2) {
+      // ----------------------- the next items' queries, half a tile a warp
+      // (each warp stands for two of the softmax warps' four arrivals).
+      uint32_t i = 1;
+      for (uint32_t w = blockIdx.x + gridDim.x; w < items; w += gridDim.x, ++i) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(q_empty, (i - 1) & 1))) {
+          if (lane == 0) atomicOr(a.err, kErrProducerWait);
+          break;
+        }
+        const Item it = place_item(a, w);
+        load_queries<kD16, 2>(a, it, sq, 2 * (warp - kSoft - 2), lane);
+        if (lane == 0) {
+          mbar_arrive(q_full);
+          mbar_arrive(q_full);
         }
       }
     }
-    if (warp > kSoft && warp <= kSoft + kQT) {
-      // ------------------------------------- MMAs, a warp per query tile
+    if (warp == kSoft + 1) {
+      // ---------------------------------------------------------------- MMAs
       // Warp reductions and votes hand their results over in uniform registers.
       constexpr uint32_t kAll = 0xFFFFFFFFu;
       const uint32_t tm = __reduce_max_sync(kAll, tmem);
-      const int t = __reduce_max_sync(kAll, warp) - kSoft - 1;
       constexpr uint32_t id_o = idesc_bf16(d16);
-      const uint32_t aq = smem_addr(sq) + t * img, ak = smem_addr(sk), av = smem_addr(sv);
-      const uint32_t ts = tm + t * kKv, to = tm + kQT * kKv + t * 128;
+      const uint32_t aq = smem_addr(sq), ak = smem_addr(sk), av = smem_addr(sv);
+      const uint32_t ts = tm, to = tm + kKv;
       bool ok = true;
       uint32_t g0 = 0, i = 0, done = 0;        // tiles, items, items with tiles so far
-      for (uint32_t w = blockIdx.x; w < items && ok; w = next_item<kQT>(w, items), ++i) {
-        const Item it = item_span<kQT>(a, place_item<kQT>(a, w));
+      for (uint32_t w = blockIdx.x; w < items && ok; w += gridDim.x, ++i) {
+        const Item it = item_span(a, place_item(a, w));
         const int n = __reduce_max_sync(kAll, it.n), span = __reduce_max_sync(kAll, it.end - it.begin);
         auto words = [&](int j) { return min(4, (span - j * kKv + 31) >> 5); };
         if (elect_one()) {
@@ -607,9 +581,9 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
 #pragma unroll
             for (int k = 0; k < d16 / 16; ++k)
               mma_ss(ts, panel_desc<kD16>(aq, k), panel_desc<kD16>(kk, k), id, k != 0);
-            mma_commit(&s_full[t]);
+            mma_commit(s_full);
             mma_commit(&k_empty[s]);
-            if (kQT == 1 && j + 1 == n) mma_commit(q_empty);
+            if (j + 1 == n) mma_commit(q_empty);
           };
           // K steps (16 positions) first .. first + 3 of the second product.
           auto output = [&](int s, int first, int n_k, bool fresh) {
@@ -626,9 +600,9 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
           // The last item's weights have been multiplied in their order before
           // these scores take their place; its O is read by the warps that then
           // make this one's first weights.
-          ok = mbar_spin(&q_full[t], i & 1);
+          ok = mbar_spin(q_full, i & 1);
           if (n == 0) {
-            if (kQT == 1) mbar_arrive(q_empty);
+            mbar_arrive(q_empty);
           } else {
             ok = ok && mbar_spin(&k_full[g0 % kStages], (g0 / kStages) & 1);
             tmem_fence_after();
@@ -641,11 +615,11 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
             // stage the next K follows the end of these scores' products.
             ok = mbar_spin(&v_full[s], (g / kStages) & 1);
             if (j + 1 < n) ok = ok && mbar_spin(&k_full[(g + 1) % kStages], ((g + 1) / kStages) & 1);
-            ok = ok && mbar_spin(&p_half[2 * t], g & 1);
+            ok = ok && mbar_spin(&p_half[0], g & 1);
             if (!ok) break;
             tmem_fence_after();
             output(s, 0, min(steps, 4), j == 0);
-            if (!(ok = mbar_spin(&p_half[2 * t + 1], g & 1))) break;
+            if (!(ok = mbar_spin(&p_half[1], g & 1))) break;
             tmem_fence_after();
             output(s, 4, steps - 4, false);
             mma_commit(&v_empty[s]);
@@ -657,42 +631,39 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
           // Every MMA of the item has completed before its epilogue.  (An item without
           // tiles has no MMA to wait for, and its softmax warps do not: with a phase
           // of its own, this thread could be two ahead of them.)
-          if (n > 0) mma_commit(&o_full[t]);
+          if (n > 0) mma_commit(o_full);
         }
         ok = __all_sync(kAll, ok);
         g0 += n;
         done += n > 0;
       }
       // And before the columns are released.
-      if (done > 0) mbar_wait(&o_full[t], (done - 1) & 1);
+      if (done > 0) mbar_wait(o_full, (done - 1) & 1);
     }
     __syncwarp();
   } else {
     // ----------------------------------------------------------- softmax
     regs_up<G::kSoftRegs>();
-    const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int row = warp * 32 + lane;
     // Not zero: a masked score, -inf, stays -inf through it.
     const float sc = fmaxf(fabsf(a.scale_log2) * kUnscale, 1e-38f);
-    const uint32_t ts = tmem + (uint32_t((warp & 3) * 32) << 16) + t * kKv;
-    const uint32_t to = tmem + (uint32_t((warp & 3) * 32) << 16) + kQT * kKv + t * 128;
+    const uint32_t ts = tmem + (uint32_t(warp * 32) << 16);
+    const uint32_t to = ts + kKv;
     bool ok = true;
     uint32_t g = 0, done = 0;                  // tiles, and items with tiles, so far
-    // The first turn is tile 0's.
-    if (t == 1 && item_span<kQT>(a, place_item<kQT>(a, blockIdx.x)).n > 0) next_turn<kQT>(warp);
-    for (uint32_t w = blockIdx.x; w < items; w = next_item<kQT>(w, items)) {
-      const Item it = item_span<kQT>(a, place_item<kQT>(a, w));
-      const int r = it.r0 + t * kQr + row;
+    for (uint32_t w = blockIdx.x; w < items; w += gridDim.x) {
+      const Item it = item_span(a, place_item(a, w));
+      const int r = it.r0 + row;
       const bool mine = r < a.rows;
       const int m = mine ? a.group.div(r) : 0, h = it.hk * a.group.d + (mine ? r - m * a.group.d : 0);
       const int limit = row_limit(a, it.len, r);
-      const int tile_limit = row_limit(a, it.len, min(it.r0 + t * kQr, a.rows - 1));   // the fewest of the tile
+      const int tile_limit = row_limit(a, it.len, it.r0);      // the fewest of the tile
       float mx = -INFINITY, l = 0.0f;
       const uint4* mask = a.tile_mask + it.b * a.tiles + it.begin / kKv;
       const int n = it.n;
-      int j = 0;
-      for (; j < n && ok; ++j, ++g) {
+      for (int j = 0; j < n; ++j, ++g) {
         const uint4 there = __ldg(mask + j);
-        ok = __all_sync(0xFFFFFFFFu, mbar_spin(&s_full[t], g & 1));
+        ok = __all_sync(0xFFFFFFFFu, mbar_spin(s_full, g & 1));
         if (!ok) break;
         tmem_fence_after();
         const int pos0 = it.begin + j * kKv;
@@ -704,24 +675,15 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
             const int left = limit - pos0 - 32 * v;          // positions of this word the row sees
             see[v] = left >= 32 ? see[v] : left <= 0 ? 0u : see[v] & ((1u << left) - 1u);
           }
-          softmax_tile<false, kD16, kQT>(ts, to, sc, mx, l, j == 0, see, words, p_half + 2 * t, warp, lane,
-                                          t == 1 && j + 1 == n);
+          softmax_tile<false, kD16>(ts, to, sc, mx, l, j == 0, see, words, p_half, lane);
         } else {
-          softmax_tile<true, kD16, kQT>(ts, to, sc, mx, l, j == 0, see, 4, p_half + 2 * t, warp, lane,
-                                          t == 1 && j + 1 == n);
+          softmax_tile<true, kD16>(ts, to, sc, mx, l, j == 0, see, 4, p_half, lane);
         }
       }
-      if (!ok) {
-        // Gave up: the other tile's turns go on.
-        for (; j < n; ++j) {
-          my_turn<kQT>(warp);
-          if (t == 0 || j + 1 < n) next_turn<kQT>(warp);
-        }
-        continue;
-      }
-      if (n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&o_full[t], done & 1));
+      if (!ok) break;
+      if (n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_full, done & 1));
       done += n > 0;
-      if (!ok) continue;
+      if (!ok) break;
       tmem_fence_after();
       const bool part = a.n_chunks > 1;
       const int64_t at = ((it.b * a.view.heads + it.hk) * a.n_chunks + it.chunk) * a.rows + r;
@@ -784,25 +746,25 @@ __global__ void __launch_bounds__(TcGeom<kQT, kD16>::kThreads, kQT == 2 ? 1 : 2)
 
 // setmaxnreg draws on what the block was launched with: were that less than the
 // warpgroups' shares, the kernel would wait for good.
-template <int kQT, int kD16>
+template <int kD16>
 bool registers_suffice() {
-  using G = TcGeom<kQT, kD16>;
-  static const int regs = launched_regs(attn_tc_kernel<kQT, kD16>);
-  return regs * (kQT + 1) >= kQT * G::kSoftRegs + G::kRestRegs;
+  using G = TcGeom<kD16>;
+  static const int regs = launched_regs(attn_tc_kernel<kD16>);
+  return regs * 2 >= G::kSoftRegs + G::kRestRegs;
 }
 
-template <int kQT, int kD16>
+template <int kD16>
 int launch_tc(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
-  using G = TcGeom<kQT, kD16>;
-  const int rc = allow_smem<attn_tc_kernel<kQT, kD16>>(G::kSmem, dev);
+  using G = TcGeom<kD16>;
+  const int rc = allow_smem<attn_tc_kernel<kD16>>(G::kSmem, dev);
   if (rc != KQ_OK) return rc;
-  if (!registers_suffice<kQT, kD16>()) return record_cuda_error(cudaErrorLaunchOutOfResources);
-  const int64_t items = (a.rows + kQT * kQr - 1) / (kQT * kQr) * p.n_chunks * a.view.heads * batch;
+  if (!registers_suffice<kD16>()) return record_cuda_error(cudaErrorLaunchOutOfResources);
+  const int64_t items = (a.rows + kQr - 1) / kQr * p.n_chunks * a.view.heads * batch;
   if (items > (int64_t(1) << 31) - 65536) return KQ_ERR_INVALID;
-  // One query tile: the blocks that are resident at once take the items in turn,
-  // the next one's queries and keys on their way under the last one's output.
-  const int64_t grid = kQT == 1 ? std::min<int64_t>(items, 2 * 148) : items;
-  const cudaError_t e = launch_pdl(attn_tc_kernel<kQT, kD16>, dim3(static_cast<unsigned>(grid)),
+  // The blocks that are resident at once take the items in turn, the next one's
+  // queries and keys on their way under the last one's output.
+  const int64_t grid = std::min<int64_t>(items, 2 * 148);
+  const cudaError_t e = launch_pdl(attn_tc_kernel<kD16>, dim3(static_cast<unsigned>(grid)),
                                    dim3(G::kThreads), G::kSmem, st, a,
                                    static_cast<uint32_t>(items));
   return e == cudaSuccess ? KQ_OK : record_cuda_error(e);
@@ -810,7 +772,7 @@ int launch_tc(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cuda
 
 template <int kD16>
 int launch_tc_qt(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
-  return p.q_tiles == 2 ? launch_tc<2, kD16>(a, p, batch, dev, st) : launch_tc<1, kD16>(a, p, batch, dev, st);
+  return launch_tc<kD16>(a, p, batch, dev, st);
 }
 
 }  // namespace

@@ -493,7 +493,7 @@ AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_le
   const int64_t images = batch * kv_heads * p.tiles * 512 * d16;
   // Up to 64 rows the split kernel's passes over the codes (one for 32 rows) cost
   // less than decoding the cache to memory: 8 x 8 heads of 128 over 16384
-  // positions, 64 rows 235 against 295 us, 96 rows 328 against 301.  Past 4 GiB of
+  // positions, 64 rows 242 against 291 us, 96 rows 345 against 297.  Past 4 GiB of
   // decoded tiles it serves any number of rows.
   p.tensor_core = rows > 64 && images <= (int64_t(1) << 32) && kv_heads < 32768;
   if (p.tensor_core) {

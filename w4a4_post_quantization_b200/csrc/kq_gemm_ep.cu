@@ -37,6 +37,10 @@ constexpr int kBoxRows = 32;
 constexpr int kBoxBytes = kBoxRows * 128;
 constexpr int kEpStaging = 65536;             // the epilogue warps' boxes
 
+// Registers a thread: wide tiles have 20 warps, launched with 96, of which the
+// epilogue's take 104 and the others keep 64.
+constexpr int kEpRegs = 104, kRestRegs = 64;
+
 template <int kN>
 struct EpGeom {
   static constexpr int kStages = kN == 256 ? 4 : 6;
@@ -44,10 +48,7 @@ struct EpGeom {
   static constexpr int kWarps = kN / 16;      // epilogue warps
   static constexpr int kThreads = 32 * (kWarps + 4);
   static constexpr int kSlots = kEpStaging / kBoxBytes / kWarps;   // boxes per warp
-  // Registers a thread: wide tiles have 20 warps, launched with 96, of which the
-  // epilogue's take 104 and the others keep 64.
-  static constexpr bool kSplit = kN == 256;
-  static constexpr int kEpRegs = 104, kRestRegs = 64;
+  static constexpr bool kSplit = kN == 256;   // registers shared out as above
   static constexpr int kVectors = kWarps * 2 * kCols * 4;   // bias and gate of each warp's columns
   static constexpr int kSmem = 1024 + kStages * P::kStage + kEpStaging + kVectors +
                                (2 * kStages + 2 * P::kAcc + kWarps) * 8 + 16;
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(EpGeom<kN>::kThreads, 1)
   pdl_wait_then_trigger();
 
   if (warp >= E::kWarps) {
-    if constexpr (E::kSplit) regs_down<E::kRestRegs>();
+    if constexpr (E::kSplit) regs_down<kRestRegs>();
     const uint32_t tm = __reduce_max_sync(0xFFFFFFFFu, tmem_base);       // uniform
     if (warp == E::kWarps) {
       if (elect_one() && !pair_produce<kN, kStages>(base, full, empty, &amap, &bmap, &sfamap, &sfbmap,
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(EpGeom<kN>::kThreads, 1)
         atomicOr(a.err, kErrConsumerWait);
     }
   } else {
-    if constexpr (E::kSplit) regs_up<E::kEpRegs>();
+    if constexpr (E::kSplit) regs_up<kEpRegs>();
     constexpr int kGroups = kCols / 32;           // 32-column groups of a thread
     constexpr int kBoxCols = kBf16 ? 64 : 32;
     constexpr int kBoxes = kCols / kBoxCols;      // boxes of a warp and tile
@@ -484,7 +485,7 @@ int launch_ep(const EpCall& c, EpArgs a) {
     // setmaxnreg draws on what the block was launched with: were that less than
     // the warps' shares, the kernel would wait for good.
     static const int regs = launched_regs(gemm_mxf4_ep<kN, kBf16, kAct>);
-    if (regs * (E::kWarps + 4) < E::kEpRegs * E::kWarps + E::kRestRegs * 4)
+    if (regs * (E::kWarps + 4) < kEpRegs * E::kWarps + kRestRegs * 4)
       return record_cuda_error(cudaErrorLaunchOutOfResources);
   }
   return launch_pairs<gemm_mxf4_ep<kN, kBf16, kAct>>(

@@ -196,6 +196,25 @@ def test_many_sequences_with_empty_ones_among_them(M, Hkv, D, causal, empty):
     run(B, M, Hkv, Hkv, D, 150, 32, lens, causal, seed=empty)
 
 
+def test_very_long_sequences_one_after_another():
+    """More tiles of rows than a GPU holds at once, so that a block takes a second
+    one after 4 million positions of the first.  Flat weights and values of 1: every
+    sum is a whole number below 2^24, and the result exactly 1."""
+    L, M, page = 1 << 22, 128 * 300, 1024
+    cache = kq.cache_alloc(L // page, page, 1, 16, device=DEV)
+    rng = np.random.default_rng(3)
+    cache.k_codes.copy_(torch.from_numpy(rng.integers(0, 256, tuple(cache.k_codes.shape), dtype=np.uint8)))
+    cache.k_scales.fill_(127)
+    cache.v_codes.fill_(0x22)                                # 1.0 and 1.0
+    cache.v_scales.fill_(127)
+    table = torch.arange(L // page, dtype=torch.int32, device=DEV).view(1, -1)
+    q = torch.zeros((1, M, 1, 16), dtype=torch.bfloat16, device=DEV)
+    out = torch.full_like(q, float("nan"))
+    kq.attention_mxfp4(q, cache, table, i32([L]), out=out)
+    assert kq.device_status() == 0
+    assert bool((out == 1).all())
+
+
 @pytest.mark.parametrize("M", [1, 140])
 def test_max_len_bounds_lens(M):
     """Lengths above max_len count as max_len, negative ones as 0."""

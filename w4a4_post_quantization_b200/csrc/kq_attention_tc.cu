@@ -545,7 +545,12 @@ __global__ void __launch_bounds__(TcGeom<kD16>::kThreads, 2)
       // (each warp stands for two of the softmax warps' four arrivals).
       uint32_t i = 1;
       for (uint32_t w = blockIdx.x + gridDim.x; w < items; w += gridDim.x, ++i) {
-        if (!__all_sync(0xFFFFFFFFu, mbar_wait(q_empty, (i - 1) & 1))) {
+        // The one wait that lasts an item, of up to half a million tiles: its bound
+        // grows with them (a wait gives up after some 20 ms, 512 tiles take under one).
+        bool ok = false;
+        for (int left = item_span(a, place_item(a, w - gridDim.x)).n; !ok && left >= 0; left -= 512)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_empty, (i - 1) & 1));
+        if (!ok) {
           if (lane == 0) atomicOr(a.err, kErrProducerWait);
           break;
         }

@@ -353,3 +353,16 @@ def test_refusals():
         call(q, cache, table, lens, scale=float("nan"))
     empty = call(q[:, :0], cache, table, lens)
     assert empty.shape == (2, 0, 4, 64)
+
+
+def test_output_over_the_queries_is_refused():
+    cache, table, k, v = make_cache(2, 32, 2, 64, 16, 19)
+    both = torch.zeros((3, 2, 3, 4, 64), dtype=torch.bfloat16, device=DEV)
+    q, lens = both[0], i32([32, 32])
+    for out in (q, both.flatten()[64 : 64 + q.numel()].view(q.shape)):
+        with pytest.raises(ValueError):
+            kq.attention_mxfp4(q, cache, table, lens, out=out)
+    kq.attention_mxfp4(q, cache, table, lens, out=both[1])
+    fused = torch.zeros((2, 3, 2, 4, 64), dtype=torch.bfloat16, device=DEV)
+    kq.attention_mxfp4(fused[:, :, 0], cache, table, lens, out=fused[:, :, 1])
+    torch.cuda.synchronize()

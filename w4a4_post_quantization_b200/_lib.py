@@ -726,7 +726,8 @@ def attention_mxfp4(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     last M of them); heads / cache.heads query heads read one K/V head.  scale
     defaults to head_dim^-0.5, max_len (a bound on lens) to what the block table
     holds.  lse: an optional float32 [batch, heads, M] output.  A row that sees
-    no position gives 0, and -inf in lse.  Returns bf16 like q."""
+    no position gives 0, and -inf in lse.  out must not share memory with q.
+    Returns bf16 like q."""
     if lens is None:
         raise ValueError("lens must be int32 [batch]")
     return (_BINDING or _binding()).attention(q, cache._ptr, cache._index, block_table, lens, causal,

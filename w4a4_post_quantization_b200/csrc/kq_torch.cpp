@@ -293,6 +293,11 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto os = head_rows(out, at::kBFloat16, c.dev, "out");
     if (out.sizes() != q.sizes()) refuse("out must have the shape of q");
     disjoint(out, "out");
+    if (given && q.numel() > 0) {
+      const intptr_t d = static_cast<char*>(given->data_ptr()) - static_cast<char*>(q.data_ptr());
+      const bool dense = q.is_contiguous() && given->is_contiguous();
+      if (d == 0 || (dense && std::abs(d) < static_cast<intptr_t>(q.nbytes()))) refuse("out and q must not share memory");
+    }
     const at::Tensor* lse = tensor(a[9], "lse", true);
     if (lse) {
       check_dense(*lse, at::kFloat, c.dev, "lse");

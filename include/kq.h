@@ -279,8 +279,8 @@ enum {
  *   of each sample (tokens_per_sample >= 1 where there is a gate); residual:
  *   [M][N] of c's type, which may be c itself (c += ...) and must not overlap it
  *   otherwise.  All 16-byte aligned; operands, c and c_dtype as for
- *   kq_gemm_mxfp4_tiled, M, N and K below 2^31 - 512.  Rows whose N is a
- *   multiple of 8 take the fast path out.  An activation is within 2e-6 times
+ *   kq_gemm_mxfp4_tiled, M and N below 2^31 - 512, K at most 2^21.  Rows whose N is
+ *   a multiple of 8 take the fast path out.  An activation is within 2e-6 times
  *   the larger of |y| and 1 of its value at the float32 y. */
 int kq_gemm_mxfp4_epilogue(const uint8_t* qa, const uint8_t* sa_tiled, const uint8_t* qb,
                            const uint8_t* sb_tiled, int64_t M, int64_t N, int64_t K,

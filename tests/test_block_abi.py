@@ -134,3 +134,7 @@ def test_bad_epilogue(L, bad):
 
 def test_empty_epilogue_needs_no_device(L):
     assert epilogue(L, M=0, qa=None, c=None) == 0 and epilogue(L, N=0, qb=None, c=None) == 0
+
+
+def test_epilogue_bound_of_k(L):
+    assert epilogue(L, K=(1 << 21) + 32) == 1

@@ -179,6 +179,19 @@ def test_a_whole_output_stays_inside_its_rows():
         assert torch.equal(out, kq.gemm_mxfp4_epilogue(*args))
 
 
+def test_the_longest_product():
+    """2^21 products of ones a sum: exact in float32.  One more block is refused."""
+    M, N, K = 4, 8, 1 << 21
+    s = torch.full((128 * (K // 32) + 512,), 127, dtype=torch.uint8, device=DEV)   # one tile of 128 rows
+    qa, qb = (torch.full((r, K // 2), 0x22, dtype=torch.uint8, device=DEV) for r in (M, N))
+    out = kq.gemm_mxfp4_epilogue(qa, s[:-512], qb, s[:-512], out_dtype=torch.float32)
+    assert kq.device_status() == 0
+    assert bool((out == K).all())
+    longer = [torch.full((r, K // 2 + 16), 0x22, dtype=torch.uint8, device=DEV) for r in (M, N)]
+    with pytest.raises((ValueError, kq.KQError)):
+        kq.gemm_mxfp4_epilogue(longer[0], s, longer[1], s)
+
+
 def test_empty_and_refusals():
     e = torch.empty((0, 32), dtype=torch.uint8, device=DEV)
     s0 = torch.empty((0,), dtype=torch.uint8, device=DEV)

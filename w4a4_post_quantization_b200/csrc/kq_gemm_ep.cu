@@ -533,7 +533,10 @@ extern "C" int kq_gemm_mxfp4_epilogue(const uint8_t* qa, const uint8_t* sa_tiled
   if (gate && tokens_per_sample < 1) return KQ_ERR_INVALID;
   if (M == 0 || N == 0) return KQ_OK;
   constexpr int64_t kMost = (int64_t(1) << 31) - 2 * kBK;
-  if (M > kMost || N > kMost || K > kMost) return KQ_ERR_INVALID;
+  // The epilogue waits for a whole product along K, and gives up after 10 to 30 ms:
+  // 2^21 is 8192 stages of at most about 1 us.  (A bound that grows with K cost
+  // 1.4 us of 34 at 8192 x 4608 x 1152, GELU.)
+  if (M > kMost || N > kMost || K > (int64_t(1) << 21)) return KQ_ERR_INVALID;
   if (((M + kPairM - 1) / kPairM) * ((N + 127) / 128) > (int64_t(1) << 31) - 65536) return KQ_ERR_INVALID;
   auto al = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };
   if (!qa || !sa_tiled || !qb || !sb_tiled || !c) return KQ_ERR_INVALID;

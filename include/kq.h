@@ -376,7 +376,9 @@ int kq_cache_read(const kq_cache* cache, const int32_t* block_table, int64_t bat
  *   out[b][m][h] = sum_p softmax_p(scale q[b][m][h] . K[p]) V[p]
  * over p < len[b], with causal != 0 also p <= len[b] - M + m (the queries are
  * the last M positions); head h reads K/V head h / (heads / kv heads).  A row
- * that sees no position has out = 0 and lse = -inf.
+ * that sees no position has out = 0 and lse = -inf, whatever its queries are; any
+ * other row with a NaN or an infinity among its queries has out and lse NaN (no
+ * other row is affected).
  *   q: bf16, element (b, m, h, c) at b * q_sb + m * q_sm + h * q_sh + c;
  *   out: bf16 with strides o_*; pointers 16-byte aligned, strides non-negative
  *   multiples of 8.  out must not overlap q.

@@ -6,6 +6,11 @@
 // The positions are walked once with the running maximum and sum of the
 // softmax, all of them float32; a row that sees no position has O = 0 and a
 // log-sum-exp of -inf.
+//
+// A query with a NaN or an infinity has no finite score (the cache holds finite
+// values), and maxima drop NaN: its maximum can be -inf, as that of a row that sees
+// nothing.  The sum tells them apart: it is NaN where a score is NaN or +inf, and 0
+// where nothing is seen; one whose scores are all -inf is made NaN (row_sees).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -76,6 +81,14 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// Whether there is a page for any position of [begin, end).  Asked only of a row
+// whose sum is 0.
+__device__ __forceinline__ bool row_sees(const AttnArgs& a, int64_t b, int begin, int end) {
+  for (int64_t pos = begin; pos < end; pos += int64_t(1) << a.view.page_shift)
+    if (cache_row(a.view, b, pos, 0) >= 0) return true;
+  return end > begin && cache_row(a.view, b, end - 1, 0) >= 0;
 }
 
 // kNT: groups of 8 query rows.
@@ -406,20 +419,19 @@ __global__ void __launch_bounds__(32 * kWarps, kNT == 1 ? 4 : kNT == 2 ? 3 : 2)
       sum += k * ml.y;
       acc.x += k * x.x, acc.y += k * x.y, acc.z += k * x.z, acc.w += k * x.w;
     }
+    if (sum == 0.0f && row_sees(a, b, begin, min(end, row_limit(a, len, r0 + r)))) sum = kNaN;
     if (a.n_chunks > 1) {
       const int64_t at = ((b * a.view.heads + hk) * a.n_chunks + chunk) * a.rows + r0 + r;
-      if (top != -INFINITY) *reinterpret_cast<float4*>(a.part_o + at * G::kDp + d) = acc;
+      if (sum != 0.0f) *reinterpret_cast<float4*>(a.part_o + at * G::kDp + d) = acc;
       if (d == 0) a.part_ml[at] = make_float2(top, sum);
       continue;
     }
     const int m = a.group.div(r0 + r), h = hk * a.group.d + r0 + r - m * a.group.d;
-    const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+    const float inv = unscale(sum);
     if (d < a.D)
       *reinterpret_cast<uint2*>(a.out + b * a.ob + m * a.om + h * a.oh + d) =
           make_uint2(bf16x2(acc.x * inv, acc.y * inv), bf16x2(acc.z * inv, acc.w * inv));
-    if (a.lse && d == 0)
-      a.lse[(b * a.view.heads * a.group.d + h) * a.M + m] =
-          top == -INFINITY ? -INFINITY : (top + (log2f(sum) - kShift)) * kLn2;
+    if (a.lse && d == 0) a.lse[(b * a.view.heads * a.group.d + h) * a.M + m] = row_lse(top, sum);
   }
 }
 
@@ -441,7 +453,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int64_
   const float* po = a.part_o + (bh * a.n_chunks * a.rows + r) * (32 * kW) + 32 * j + lane;
   const int64_t step = static_cast<int64_t>(a.rows) * (32 * kW);
   // The first chunks' O is on its way while the weights are worked out; O of a
-  // chunk in which the row sees nothing has not been written, and is not used.
+  // chunk in which the row sees nothing has not been written, and is not used (its
+  // sum is 0; a NaN sum makes the whole row NaN).
   constexpr int kAhead = 8;
   float x[kAhead];
   auto fetch = [&](int i0) {
@@ -477,12 +490,11 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnArgs a, int64_
     }
   }
   const int m = a.group.div(r), h = hk * a.group.d + r - m * a.group.d;
-  const float inv = sum > 0.0f ? kUnscale / sum : 0.0f;
+  const float inv = unscale(sum);
   if (32 * j + lane < a.D)
     a.out[b * a.ob + m * a.om + h * a.oh + 32 * j + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(acc * inv));
   if (a.lse && j == 0 && lane == 0)
-    a.lse[(b * a.view.heads * a.group.d + h) * a.M + m] =
-        top == -INFINITY ? -INFINITY : (top + (log2f(sum) - kShift)) * kLn2;
+    a.lse[(b * a.view.heads * a.group.d + h) * a.M + m] = row_lse(top, sum);
 }
 
 AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_len, int64_t head_dim) {

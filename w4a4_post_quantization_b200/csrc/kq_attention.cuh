@@ -13,6 +13,7 @@
 namespace kq {
 
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNaN = __builtin_nanf("");
 
 struct AttnArgs {
   CacheView view;
@@ -92,6 +93,14 @@ __device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&p)[4]) {
 __device__ __forceinline__ uint32_t mx_mul(uint32_t s) { return (s + 64) << 7; }
 constexpr int kShift = 62;
 constexpr float kUnscale = 4611686018427387904.0f;      // 2^kShift
+
+// Out of a row's maximum and sum of weights: the factor that makes its accumulator
+// the output, and its log-sum-exp.  A sum of 0 is a row that sees nothing, a NaN one
+// that is not a number; the maximum, which drops NaN, is -inf in both.
+__device__ __forceinline__ float unscale(float sum) { return sum == 0.0f ? 0.0f : kUnscale / sum; }
+__device__ __forceinline__ float row_lse(float top, float sum) {
+  return sum == 0.0f ? -INFINITY : (top + (log2f(sum) - kShift)) * kLn2;
+}
 
 // How a call is cut: from its sizes alone, so that the workspace query and the
 // call agree.

@@ -325,6 +325,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sc,
     const float alpha = m_new == -INFINITY ? 1.0f : ex2(mx - m_new);
     mx = m_new;
     l *= alpha;
+    if (mx == INFINITY) l = kNaN;
     // These scores were issued after the last weights' product, so O is
     // complete.
     if (!first) {
@@ -339,6 +340,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float sc,
       }
     }
   }
+  // A row that sees positions and has no score above -inf so far is not a number.
+  // (Its sum would not always show it: the polynomial has a least value.)
+  if (mx == -INFINITY && (kWhole || (see[0] | see[1] | see[2] | see[3]) != 0)) l = kNaN;
   const float shift = kShift - (mx == -INFINITY ? 0.0f : mx);
   const f2 sc2 = pack2(sc, sc), shift2 = pack2(shift, shift);
   f2 sum[2] = {pack2(0.0f, 0.0f), pack2(0.0f, 0.0f)};
@@ -692,7 +696,7 @@ __global__ void __launch_bounds__(TcGeom<kD16>::kThreads, 2)
       tmem_fence_after();
       const bool part = a.n_chunks > 1;
       const int64_t at = ((it.b * a.view.heads + it.hk) * a.n_chunks + it.chunk) * a.rows + r;
-      const float inv = l > 0.0f ? kUnscale / l : 0.0f;
+      const float inv = unscale(l);
       float* po = a.part_o + at * (32 * a.view.nb);
       uint16_t* out = a.out + it.b * a.ob + m * a.om + h * a.oh;
       // 32 channels at a time.  (Through shared memory, four lanes to a row's 64 bytes:
@@ -709,7 +713,7 @@ __global__ void __launch_bounds__(TcGeom<kD16>::kThreads, 2)
           if (c + 16 < d16) tmem_ld16(to + c + 16, o[1]);
           tmem_wait_ld();
         }
-        if (mine && part && mx != -INFINITY) {
+        if (mine && part && l != 0.0f) {
 #pragma unroll
           for (int u = 0; u < 2; ++u)
             if (c + 16 * u < d16)
@@ -734,8 +738,7 @@ __global__ void __launch_bounds__(TcGeom<kD16>::kThreads, 2)
       }
       if (mine && part) a.part_ml[at] = make_float2(mx, l);
       if (mine && !part && a.lse)
-        a.lse[(it.b * a.view.heads * a.group.d + h) * a.M + m] =
-            mx == -INFINITY ? -INFINITY : (mx + (log2f(l) - kShift)) * kLn2;
+        a.lse[(it.b * a.view.heads * a.group.d + h) * a.M + m] = row_lse(mx, l);
       // O has been read: the next item's first weights come after.
       tmem_fence_before();
     }

@@ -647,10 +647,11 @@ class KVCache:
     """A pool of MXFP4 K/V pages: codes uint8 [pages, heads, page_size, Dp/2]
     and scale bytes uint8 [pages, heads, page_size, Dp/32] for K and for V, Dp =
     head_dim rounded up to 32.  Holds the caller's tensors; ``cache_alloc``
-    makes new ones."""
+    makes new ones.  Its attributes cannot be assigned, and the calls refuse a cache
+    whose tensors have been resized or given other memory: another pool (a grown one,
+    say) is another KVCache."""
 
-    __slots__ = ("k_codes", "k_scales", "v_codes", "v_scales", "pages", "page_size", "heads",
-                 "head_dim", "device", "_c", "_ptr", "_index")
+    __slots__ = ("_tensors", "_c", "_ptr", "_index")
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
                  v_scales: torch.Tensor, head_dim: int):
@@ -672,14 +673,21 @@ class KVCache:
             raise ValueError("page_size must be a power of two from 16 to 65536")
         if pages < 1 or heads < 1:
             raise ValueError("the cache needs a page and a head")
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = \
-            k_codes, k_scales, v_codes, v_scales
-        self.pages, self.page_size, self.heads, self.head_dim = pages, page_size, heads, head_dim
-        self.device = k_codes.device
-        self._c = _CacheStruct(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
-                               v_scales.data_ptr(), pages, page_size, heads, head_dim)
+        self._tensors = (k_codes, k_scales, v_codes, v_scales)
+        self._c = _CacheStruct(*(t.data_ptr() for t in self._tensors), pages, page_size, heads,
+                               head_dim)
         self._ptr = ctypes.addressof(self._c)
-        self._index = self.device.index
+        self._index = k_codes.device.index
+
+    k_codes = property(lambda self: self._tensors[0])
+    k_scales = property(lambda self: self._tensors[1])
+    v_codes = property(lambda self: self._tensors[2])
+    v_scales = property(lambda self: self._tensors[3])
+    pages = property(lambda self: self._c.pages)
+    page_size = property(lambda self: self._c.page_size)
+    heads = property(lambda self: self._c.heads)
+    head_dim = property(lambda self: self._c.head_dim)
+    device = property(lambda self: self._tensors[0].device)
 
 
 def cache_alloc(pages: int, page_size: int, heads: int, head_dim: int, device="cuda") -> KVCache:
@@ -697,7 +705,8 @@ def cache_write(cache: KVCache, block_table: torch.Tensor, k: torch.Tensor, v: t
     bf16 k and v [batch, tokens, heads, head_dim] goes to position start[b] + t
     (default: t) of sequence b, page block_table[b, position // page_size].
     Everything else in the cache stays as it was."""
-    (_BINDING or _binding()).cache_write(cache._ptr, cache._index, block_table, k, v, start, lens)
+    (_BINDING or _binding()).cache_write(cache._ptr, cache._index, cache._tensors, block_table, k, v,
+                                         start, lens)
     return cache
 
 
@@ -708,8 +717,8 @@ def cache_read(cache: KVCache, block_table: torch.Tensor, lens, tokens: int, sta
     the others are zeros."""
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
-    return (_BINDING or _binding()).cache_read(cache._ptr, cache._index, block_table, lens, tokens,
-                                               start, out_dtype is torch.float32, k, v)
+    return (_BINDING or _binding()).cache_read(cache._ptr, cache._index, cache._tensors, block_table,
+                                               lens, tokens, start, out_dtype is torch.float32, k, v)
 
 
 def attention_workspace_bytes(batch: int, M: int, heads: int, kv_heads: int, head_dim: int,
@@ -732,8 +741,8 @@ def attention_mxfp4(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     Returns bf16 like q."""
     if lens is None:
         raise ValueError("lens must be int32 [batch]")
-    return (_BINDING or _binding()).attention(q, cache._ptr, cache._index, block_table, lens, causal,
-                                              scale, max_len, out, lse, workspace)
+    return (_BINDING or _binding()).attention(q, cache._ptr, cache._index, cache._tensors, block_table,
+                                              lens, causal, scale, max_len, out, lse, workspace)
 
 
 def inverse_transform(y: torch.Tensor, params: torch.Tensor, x=None):

@@ -115,8 +115,18 @@ struct CacheRef {
   const kq_cache* c;
   int64_t dev;
 };
-CacheRef cache_ref(PyObject* address, PyObject* device) {
-  return {reinterpret_cast<const kq_cache*>(integer(address, "cache")), integer(device, "device")};
+// The cache's description, and its four tensors: what the description points to must
+// still be theirs.
+CacheRef cache_ref(PyObject* address, PyObject* device, PyObject* tensors) {
+  const kq_cache* c = reinterpret_cast<const kq_cache*>(integer(address, "cache"));
+  const void* at[4] = {c->k_codes, c->k_scales, c->v_codes, c->v_scales};
+  const size_t rows = static_cast<size_t>(c->pages * c->heads * c->page_size), nb = (c->head_dim + 31) / 32;
+  for (int i = 0; i < 4; ++i) {
+    const at::Tensor& t = *tensor(PyTuple_GET_ITEM(tensors, i), "the cache's arrays");
+    if (t.data_ptr() != at[i] || t.storage().nbytes() < t.storage_offset() + rows * nb * (i & 1 ? 1 : 16))
+      refuse("the cache's tensors have been resized or given other memory: make a new KVCache");
+  }
+  return {c, integer(device, "device")};
 }
 
 const at::Tensor& check_table(PyObject* o, const CacheRef& c, int64_t batch) {
@@ -211,18 +221,18 @@ PyObject* epilogue(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (cache, device, block_table, k, v, start, lens)
+// (cache, device, tensors, block_table, k, v, start, lens)
 PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 7, [&]() -> PyObject* {
-    const CacheRef c = cache_ref(a[0], a[1]);
-    const at::Tensor &k = *tensor(a[3], "k"), &v = *tensor(a[4], "v");
+  return guarded(n, 8, [&]() -> PyObject* {
+    const CacheRef c = cache_ref(a[0], a[1], a[2]);
+    const at::Tensor &k = *tensor(a[4], "k"), &v = *tensor(a[5], "v");
     const auto ks = head_rows(k, at::kBFloat16, c.dev, "k"), vs = head_rows(v, at::kBFloat16, c.dev, "v");
     if (v.sizes() != k.sizes()) refuse("k and v must have the same shape");
     const int64_t B = k.size(0);
     if (k.size(2) != c.c->heads || k.size(3) != c.c->head_dim) refuse("k and v must have the cache's heads and head_dim");
-    const at::Tensor& table = check_table(a[2], c, B);
-    const at::Tensor* start = check_per_seq(a[5], c, B, "start", true);
-    const at::Tensor* lens = check_per_seq(a[6], c, B, "lens", true);
+    const at::Tensor& table = check_table(a[3], c, B);
+    const at::Tensor* start = check_per_seq(a[6], c, B, "start", true);
+    const at::Tensor* lens = check_per_seq(a[7], c, B, "lens", true);
     if (!call("kq_cache_write", c.dev, [&](void* st) {
           return g.cache_write(c.c, static_cast<int32_t*>(table.data_ptr()), B, table.size(1),
                                static_cast<uint16_t*>(k.data_ptr()), ks[0], ks[1], ks[2],
@@ -234,22 +244,22 @@ PyObject* cache_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (cache, device, block_table, lens, tokens, start, f32, k, v)
+// (cache, device, tensors, block_table, lens, tokens, start, f32, k, v)
 PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 9, [&]() -> PyObject* {
-    const CacheRef c = cache_ref(a[0], a[1]);
-    const at::Tensor& table = check_table(a[2], c, -1);
-    const int64_t B = table.size(0), T = integer(a[4], "tokens");
+  return guarded(n, 10, [&]() -> PyObject* {
+    const CacheRef c = cache_ref(a[0], a[1], a[2]);
+    const at::Tensor& table = check_table(a[3], c, -1);
+    const int64_t B = table.size(0), T = integer(a[5], "tokens");
     if (T < 0) refuse("tokens must not be negative");
-    const at::Tensor* lens = check_per_seq(a[3], c, B, "lens", true);
-    const at::Tensor* start = check_per_seq(a[5], c, B, "start", true);
-    const at::ScalarType type = a[6] == Py_True ? at::kFloat : at::kBFloat16;
+    const at::Tensor* lens = check_per_seq(a[4], c, B, "lens", true);
+    const at::Tensor* start = check_per_seq(a[6], c, B, "start", true);
+    const at::ScalarType type = a[7] == Py_True ? at::kFloat : at::kBFloat16;
     const std::array<int64_t, 4> shape{B, T, c.c->heads, c.c->head_dim};
     at::Tensor x[2];
     std::array<int64_t, 3> s[2];
     for (int i = 0; i < 2; ++i) {
       const char* name = i ? "v" : "k";
-      const at::Tensor* given = tensor(a[7 + i], name, true);
+      const at::Tensor* given = tensor(a[8 + i], name, true);
       x[i] = given ? *given : at::empty(shape, table.options().dtype(type));
       s[i] = head_rows(x[i], type, c.dev, name);
       if (x[i].sizes() != at::IntArrayRef(shape)) refuse(std::string(name) + " must be [batch, tokens, heads, head_dim]");
@@ -267,28 +277,28 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (q, cache, device, block_table, lens, causal, scale, max_len, out, lse, workspace)
+// (q, cache, device, tensors, block_table, lens, causal, scale, max_len, out, lse, workspace)
 PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 11, [&]() -> PyObject* {
-    const CacheRef c = cache_ref(a[1], a[2]);
+  return guarded(n, 12, [&]() -> PyObject* {
+    const CacheRef c = cache_ref(a[1], a[2], a[3]);
     const at::Tensor& q = *tensor(a[0], "q");
     const auto qs = head_rows(q, at::kBFloat16, c.dev, "q");
     const int64_t B = q.size(0), M = q.size(1), H = q.size(2), D = q.size(3);
     if (D != c.c->head_dim || H == 0 || H % c.c->heads != 0)
       refuse("q must have the cache's head_dim and a multiple of its heads");
-    const at::Tensor& table = check_table(a[3], c, B);
-    const at::Tensor* lens = check_per_seq(a[4], c, B, "lens", false);
+    const at::Tensor& table = check_table(a[4], c, B);
+    const at::Tensor* lens = check_per_seq(a[5], c, B, "lens", false);
     const int64_t room = table.size(1) * c.c->page_size;
-    const int64_t max_len = a[7] == Py_None ? room : integer(a[7], "max_len");
+    const int64_t max_len = a[8] == Py_None ? room : integer(a[8], "max_len");
     if (max_len < 1 || max_len > room) refuse("max_len must be from 1 to what the block table holds");
-    const int causal = PyObject_IsTrue(a[5]);
+    const int causal = PyObject_IsTrue(a[6]);
     if (causal < 0) return nullptr;
     double scale = 1.0 / std::sqrt(static_cast<double>(D));
-    if (a[6] != Py_None) {
-      scale = PyFloat_AsDouble(a[6]);
+    if (a[7] != Py_None) {
+      scale = PyFloat_AsDouble(a[7]);
       if (scale == -1.0 && PyErr_Occurred()) return nullptr;
     }
-    const at::Tensor* given = tensor(a[8], "out", true);
+    const at::Tensor* given = tensor(a[9], "out", true);
     at::Tensor out = given ? *given : at::empty(q.sizes(), q.options().memory_format(at::MemoryFormat::Contiguous));
     const auto os = head_rows(out, at::kBFloat16, c.dev, "out");
     if (out.sizes() != q.sizes()) refuse("out must have the shape of q");
@@ -298,7 +308,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const bool dense = q.is_contiguous() && given->is_contiguous();
       if (d == 0 || (dense && std::abs(d) < static_cast<intptr_t>(q.nbytes()))) refuse("out and q must not share memory");
     }
-    const at::Tensor* lse = tensor(a[9], "lse", true);
+    const at::Tensor* lse = tensor(a[10], "lse", true);
     if (lse) {
       check_dense(*lse, at::kFloat, c.dev, "lse");
       if (lse->dim() != 3 || lse->size(0) != B || lse->size(1) != H || lse->size(2) != M)
@@ -306,7 +316,7 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (B > 0 && M > 0) {
       const size_t need = g.attention_workspace_bytes(B, M, H, c.c->heads, D, max_len);
-      const at::Tensor* ws = tensor(a[10], "workspace", true);
+      const at::Tensor* ws = tensor(a[11], "workspace", true);
       at::Tensor own;
       if (ws) {
         check_dense(*ws, at::kByte, c.dev, "workspace");
@@ -324,8 +334,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         return nullptr;
     }
     if (given) {
-      Py_INCREF(a[8]);
-      return a[8];
+      Py_INCREF(a[9]);
+      return a[9];
     }
     return wrap(out);
   });

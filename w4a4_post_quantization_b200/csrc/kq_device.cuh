@@ -23,7 +23,9 @@ constexpr int kErrProducerWait = 2;
 constexpr int kErrSelfTest = 4;
 
 // A bounded mbarrier wait polls at most kWaitPolls times, each poll suspending
-// for at most kWaitHintNs: about four seconds in all, far above any real wait.
+// for at most kWaitHintNs, which the hardware caps at a few microseconds: it gives up
+// after 10 to 30 ms (measured), far above the wait for a copy or for a tile's products
+// over a few thousand stages.  A wait that lasts longer work brings its own bound.
 constexpr int kWaitPolls = 4000;
 constexpr uint32_t kWaitHintNs = 1000000;
 
@@ -62,10 +64,10 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 }
 
 // Waits for the phase of the given parity to complete; gives up (returns
-// false) after kWaitPolls suspended polls.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+// false) after `polls` suspended polls.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int polls = kWaitPolls) {
   const uint32_t addr = smem_addr(bar);
-  for (int poll = 0; poll < kWaitPolls; ++poll) {
+  for (int poll = 0; poll < polls; ++poll) {
     uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"

@@ -69,6 +69,7 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int bn) {
 struct GemmArgs {
   int32_t M, N, K;
   int32_t k_tiles, m_tiles, n_tiles;
+  int32_t polls;                               // bound of the epilogue's wait (product_polls)
   int32_t sf_tiles_k, sf_tiles_n;   // tiled scales: 4-scale columns, B row tiles
   int32_t tma_store;                // the epilogue stages the tile and stores it by TMA
   int32_t sf_stride;        // scale bytes per row: K / 32
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     // ---------------------------------------------------------- epilogue
     const int quarter = warp & 3;                  // TMEM lanes 32 quarter .. +31
     const int row = m0 + quarter * 32 + lane;
-    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0));
+    const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0, a.polls));
     if (!ok) {
       if (lane == 0) atomicOr(a.err, kErrConsumerWait);
     } else if (a.tma_store) {
@@ -779,7 +780,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int b = i % P::kAcc;
       const uint32_t tb = taddr + b * kBNt;
       // One AND-barrier makes a timeout the same for the four warps.
-      const bool got = mbar_wait(&acc_full[b], (i / P::kAcc) & 1);
+      const bool got = mbar_wait(&acc_full[b], (i / P::kAcc) & 1, a.polls);
       if (!bar_and(3, 4 * 32, got)) {
         if (lane == 0) atomicOr(a.err, kErrConsumerWait);
         break;
@@ -948,7 +949,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int row0 = m0 + (int)rank * kBM;
       // One AND-barrier makes a timeout the same for the four warps, which
       // then stop (one bounded wait per failure, not one per tile).
-      ok = bar_and(3, 4 * 32, mbar_wait(acc_full, i & 1));
+      ok = bar_and(3, 4 * 32, mbar_wait(acc_full, i & 1, a.tiles.polls));
       if (!ok) break;
       tmem_fence_after();
       if (a.out_bf16) {
@@ -1057,6 +1058,7 @@ int launch_gemm_pair(const CUtensorMap& amap, const uint8_t* qb, const uint8_t* 
   PairArgs pa{};
   pa.tiles.K = g.K;
   pa.tiles.k_tiles = g.k_tiles;
+  pa.tiles.polls = g.polls;
   pa.tiles.m_tiles = (g.M + kPairM - 1) / kPairM;
   pa.tiles.n_tiles = (g.N + kBN - 1) / kBN;
   pa.out_bf16 = g.out_bf16;
@@ -1092,6 +1094,7 @@ int launch_gemm(const uint8_t* qa, const uint8_t* sa, const uint8_t* qb, const u
   a.N = static_cast<int32_t>(N);
   a.K = static_cast<int32_t>(K);
   a.k_tiles = static_cast<int32_t>((K + kBK - 1) / kBK);
+  a.polls = product_polls(a.k_tiles);
   a.m_tiles = static_cast<int32_t>((M + kBM - 1) / kBM);
   a.n_tiles = static_cast<int32_t>((N + kBN - 1) / kBN);
   a.sf_stride = static_cast<int32_t>(K / 32);

@@ -34,6 +34,11 @@ constexpr int kSfColsB = 8 * kChunksPerStage;
 constexpr int kSfCol0 = kBN;
 constexpr int kTmemCols = 512;
 
+// Polls of the wait for a whole product along K, in k_tiles stages.  A stage takes 1.2 us
+// at most (the 50 KB of every SM at once out of HBM); two polls, 2.5 us each or more, are
+// waited for it, beside the bound of every other wait.
+inline int product_polls(int64_t k_tiles) { return static_cast<int>(kWaitPolls + 2 * k_tiles); }
+
 // The same MMA over a CTA pair (M = 256): issued by the even CTA, A rows and
 // accumulator rows 0..127 in it and 128..255 in the odd one, B's N rows split
 // 128 / 128 between their shared memories, each CTA's scales in its TMEM.
@@ -106,6 +111,7 @@ struct PairGeom {
 
 struct PairTiles {
   int32_t K, k_tiles, m_tiles, n_tiles;     // tiles of 256 x kN
+  int32_t polls;                            // bound of the epilogue's wait (product_polls)
 };
 
 // Tile t of the banded order (bands of kBandN column tiles, the row tile

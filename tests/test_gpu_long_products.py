@@ -47,3 +47,11 @@ def test_the_other_kernels(monkeypatch, name, value):
     monkeypatch.setenv(name, value)
     s = unit(kq.lib().kq_scales_tiled_bytes(128, K))
     check(kq.gemm_mxfp4_tiled(ones(1, K), s, ones(8, K), s, out_dtype=torch.float32), K)
+
+
+@pytest.mark.parametrize("N,dt", [(2048, torch.bfloat16), (1024, torch.bfloat16), (1024, torch.float32)])
+def test_the_longest_with_an_epilogue_on_every_pair(N, dt):
+    """72 tiles of either width, all of whose stages share the memory's bandwidth."""
+    M, k = 9 * 256, 1 << 21
+    s = unit(kq.lib().kq_scales_tiled_bytes(M, k))
+    check(kq.gemm_mxfp4_epilogue(ones(M, k), s, ones(N, k), s, out_dtype=dt), k)

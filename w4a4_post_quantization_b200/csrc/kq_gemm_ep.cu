@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(EpGeom<kN>::kThreads, 1)
       }
       const bool one_sample = n_one;
       const int b = i % P::kAcc;
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[b], (i / P::kAcc) & 1))) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[b], (i / P::kAcc) & 1, a.tiles.polls))) {
         if (lane == 0) {
           atomicOr(a.err, kErrConsumerWait);
           // The residual's copies are in flight: let them land.
@@ -467,6 +467,7 @@ int launch_ep(const EpCall& c, EpArgs a) {
   using P = typename E::P;
   a.tiles.K = static_cast<int32_t>(c.K);
   a.tiles.k_tiles = static_cast<int32_t>((c.K + kBK - 1) / kBK);
+  a.tiles.polls = product_polls(a.tiles.k_tiles);
   a.tiles.m_tiles = static_cast<int32_t>((c.M + kPairM - 1) / kPairM);
   a.tiles.n_tiles = static_cast<int32_t>((c.N + kN - 1) / kN);
   const int64_t sf_cols = (c.K / 32 + 3) / 4;
@@ -533,9 +534,8 @@ extern "C" int kq_gemm_mxfp4_epilogue(const uint8_t* qa, const uint8_t* sa_tiled
   if (gate && tokens_per_sample < 1) return KQ_ERR_INVALID;
   if (M == 0 || N == 0) return KQ_OK;
   constexpr int64_t kMost = (int64_t(1) << 31) - 2 * kBK;
-  // The epilogue waits for a whole product along K, and gives up after 10 to 30 ms:
-  // 2^21 is 8192 stages of at most about 1 us.  (A bound that grows with K cost
-  // 1.4 us of 34 at 8192 x 4608 x 1152, GELU.)
+  // The epilogue's wait for a whole product along K lasts with its stages; 2^21 is the
+  // longest that has been run with every pair at work.
   if (M > kMost || N > kMost || K > (int64_t(1) << 21)) return KQ_ERR_INVALID;
   if (((M + kPairM - 1) / kPairM) * ((N + 127) / 128) > (int64_t(1) << 31) - 65536) return KQ_ERR_INVALID;
   auto al = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; };

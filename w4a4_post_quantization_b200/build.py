@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import glob
 import os
+import shutil
 import subprocess
 import sysconfig
 
@@ -47,11 +48,17 @@ def up_to_date() -> bool:
         _newer(BINDING, binding_sources() + [__file__])
 
 
+def _cuda_include():
+    """The headers beside nvcc, which may be a bare name or a link."""
+    nvcc = os.path.realpath(shutil.which(NVCC) or NVCC)
+    return os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
+
+
 def _binding_command():
     import torch
     from torch.utils import cpp_extension as ext
-    includes = [*ext.include_paths(), os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"),
-                sysconfig.get_paths()["include"], os.path.join(ROOT, "include")]
+    includes = [*ext.include_paths(), _cuda_include(), sysconfig.get_paths()["include"],
+                os.path.join(ROOT, "include")]
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
@@ -66,14 +73,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
     cmd = [NVCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-o", OUT + ".tmp", *sources()]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
-    binding = subprocess.Popen(_binding_command())
+    binding = failure = None
+    try:
+        binding = subprocess.Popen(_binding_command())
+    except Exception as e:                       # the library is built and installed all the same
+        failure = e
     try:
         subprocess.run(cmd, check=True)
+        os.replace(OUT + ".tmp", OUT)
     finally:
-        status = binding.wait()
+        status = binding.wait() if binding else None
+    if failure:
+        raise failure
     if status != 0:
         raise subprocess.CalledProcessError(status, binding.args)
-    os.replace(OUT + ".tmp", OUT)
     os.replace(BINDING + ".tmp", BINDING)
     return OUT
 

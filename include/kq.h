@@ -332,6 +332,9 @@ int kq_scales_to_tiled(const uint8_t* scales, int64_t rows, int64_t K, uint8_t* 
  * The four arrays are 16-byte aligned, block_table 4-byte aligned.  Values of
  * magnitude 2^60 and above, NaN and Inf are outside the contract, as are
  * scale bytes the quantizer does not write for the others.
+ * Writing and reading back keep every smaller magnitude as the quantizer does.  The
+ * attention multiplies values times 2^-62 in bf16: those of a block whose largest
+ * magnitude is 2^-68 or more exactly, others with an absolute error of at most 2^-72.
  * A row whose position is negative, lies past its table or on a page outside
  * [0, pages) is left out, and KQ_DEVERR_CACHE_INDEX is set in the device error
  * word; no other row is affected. */

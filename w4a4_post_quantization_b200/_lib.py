@@ -738,6 +738,7 @@ def attention_mxfp4(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     holds.  lse: an optional float32 [batch, heads, M] output.  A row that sees
     no position gives 0, and -inf in lse; any other row with a NaN or an infinity
     among its queries gives NaN in both.  out must not share memory with q.
+    Values of blocks below 2^-68 are taken with an absolute error of up to 2^-72.
     Returns bf16 like q."""
     if lens is None:
         raise ValueError("lens must be int32 [batch]")

@@ -85,9 +85,11 @@ __device__ __forceinline__ void e2m1_pairs(uint32_t w, uint32_t (&p)[4]) {
 }
 
 // bf16 bits of 2^(s - 63) for scale byte s <= 190: a raw code times it is the
-// value times 2^-62, exactly (2^-126 of the raw bits, 2^(s - 127) of the
-// scale).  The 2^62 keeps the multiplier in bf16's range for every scale byte
-// up to 190 (values below 2^66).  It is undone in the scores' scale, and in the
+// value times 2^-62 (2^-126 of the raw bits, 2^(s - 127) of the scale), exactly from
+// s = 57 on, where the smallest code becomes bf16's smallest number, 2^-133; below, the
+// value is off by up to 2^-72, which is half that step times 2^62, and from s = 52 on
+// down nothing is left of it.  The 2^62 keeps the multiplier in bf16's range for
+// every scale byte up to 190 (values below 2^66).  It is undone in the scores' scale, and in the
 // softmax weights, which are held as 2^62 exp2(.): their products with V then
 // have V's own range, so small weights are not lost to underflow.
 __device__ __forceinline__ uint32_t mx_mul(uint32_t s) { return (s + 64) << 7; }

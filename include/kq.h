@@ -387,6 +387,7 @@ int kq_cache_read(const kq_cache* cache, const int32_t* block_table, int64_t bat
  *   multiples of 8.  out must not overlap q.
  *   lse: float32 [batch][heads][M], the natural log-sum-exp of the scaled
  *   scores, or NULL.
+ *   scale: of magnitude below 2^65; the scaled scores, times log2(e), are float32.
  *   max_len: a bound on lens, at most table_pages * page_size and 2^30; the
  *   work is cut by it, so a tight one is faster.
  *   workspace: kq_attention_workspace_bytes(...) bytes, 256-byte aligned (NULL

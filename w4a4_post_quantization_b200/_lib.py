@@ -733,8 +733,8 @@ def attention_mxfp4(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
                     workspace=None):
     """Attention of bf16 queries [batch, M, heads, head_dim] over the first
     lens[b] positions of each sequence of the cache (causal: the queries are the
-    last M of them); heads / cache.heads query heads read one K/V head.  scale
-    defaults to head_dim^-0.5, max_len (a bound on lens) to what the block table
+    last M of them); heads / cache.heads query heads read one K/V head.  scale (below
+    2^65) defaults to head_dim^-0.5, max_len (a bound on lens) to what the block table
     holds.  lse: an optional float32 [batch, heads, M] output.  A row that sees
     no position gives 0, and -inf in lse; any other row with a NaN or an infinity
     among its queries gives NaN in both.  out must not share memory with q.

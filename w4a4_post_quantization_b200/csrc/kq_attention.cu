@@ -607,8 +607,11 @@ extern "C" int kq_attention_mxfp4(const uint16_t* q, int64_t q_sb, int64_t q_sm,
     return x >= 0 && y >= 0 && z >= 0 && x % 8 == 0 && y % 8 == 0 && z % 8 == 0;
   };
   if (!al(q, 16) || !al(out, 16) || !al(lens, 4) || !strides(q_sb, q_sm, q_sh) ||
-      !strides(o_sb, o_sm, o_sh) || (lse && !al(lse, 4)) || !std::isfinite(scale))
+      !strides(o_sb, o_sm, o_sh) || (lse && !al(lse, 4)))
     return KQ_ERR_INVALID;
+  // The kernels multiply the scores by 2^62 times this.
+  const float scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  if (!std::isfinite(scale_log2 * kUnscale)) return KQ_ERR_INVALID;
   const AttnPlan p = make_plan(batch, cache->heads, rows, max_len, cache->head_dim);
   if (p.bytes > 0 && (!al(workspace, 256) || workspace_bytes < p.bytes)) return KQ_ERR_INVALID;
   const DeviceInfo* di = nullptr;
@@ -628,7 +631,7 @@ extern "C" int kq_attention_mxfp4(const uint16_t* q, int64_t q_sb, int64_t q_sm,
   a.rows = static_cast<int32_t>(rows);
   a.causal = causal != 0;
   a.group = FastDiv(static_cast<uint32_t>(heads / cache->heads));
-  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.scale_log2 = scale_log2;
   a.chunk = static_cast<int32_t>(p.chunk);
   a.n_chunks = static_cast<int32_t>(p.n_chunks);
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -281,7 +281,7 @@ enum {
  *   otherwise.  All 16-byte aligned; operands, c and c_dtype as for
  *   kq_gemm_mxfp4_tiled, M and N below 2^31 - 512, K at most 2^21.  Rows whose N is
  *   a multiple of 8 take the fast path out.  An activation is within 2e-6 times
- *   the larger of |y| and 1 of its value at the float32 y. */
+ *   the larger of its own magnitude and 1 of its value at the float32 y. */
 int kq_gemm_mxfp4_epilogue(const uint8_t* qa, const uint8_t* sa_tiled, const uint8_t* qb,
                            const uint8_t* sb_tiled, int64_t M, int64_t N, int64_t K,
                            const uint16_t* bias, int activation, const uint16_t* gate,

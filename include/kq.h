@@ -384,7 +384,7 @@ int kq_cache_read(const kq_cache* cache, const int32_t* block_table, int64_t bat
  * other row is affected).
  *   q: bf16, element (b, m, h, c) at b * q_sb + m * q_sm + h * q_sh + c;
  *   out: bf16 with strides o_*; pointers 16-byte aligned, strides non-negative
- *   multiples of 8.  out must not overlap q.
+ *   multiples of 8.  out, lse and workspace must not overlap q or one another.
  *   lse: float32 [batch][heads][M], the natural log-sum-exp of the scaled
  *   scores, or NULL.
  *   scale: of magnitude below 2^65; the scaled scores, times log2(e), are float32.

@@ -714,7 +714,7 @@ def cache_read(cache: KVCache, block_table: torch.Tensor, lens, tokens: int, sta
                out_dtype=torch.bfloat16, k=None, v=None):
     """Rows of the cache decoded: (k, v), [batch, tokens, heads, head_dim] bf16
     or float32; row t < lens[b] (lens None: every row) is position start[b] + t,
-    the others are zeros."""
+    the others are zeros.  Given k and v must not share memory."""
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError("out_dtype must be bfloat16 or float32")
     return (_BINDING or _binding()).cache_read(cache._ptr, cache._index, cache._tensors, block_table,
@@ -737,9 +737,9 @@ def attention_mxfp4(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     2^65) defaults to head_dim^-0.5, max_len (a bound on lens) to what the block table
     holds.  lse: an optional float32 [batch, heads, M] output.  A row that sees
     no position gives 0, and -inf in lse; any other row with a NaN or an infinity
-    among its queries gives NaN in both.  out must not share memory with q.
-    Values of blocks below 2^-68 are taken with an absolute error of up to 2^-72.
-    Returns bf16 like q."""
+    among its queries gives NaN in both.  out, lse and workspace must not share
+    memory with q or one another.  Values of blocks below 2^-68 are taken with an
+    absolute error of up to 2^-72.  Returns bf16 like q."""
     if lens is None:
         raise ValueError("lens must be int32 [batch]")
     return (_BINDING or _binding()).attention(q, cache._ptr, cache._index, cache._tensors, block_table,

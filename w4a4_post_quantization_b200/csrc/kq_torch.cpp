@@ -97,18 +97,58 @@ std::array<int64_t, 3> head_rows(const at::Tensor& x, at::ScalarType type, int64
   return s;
 }
 
-// An output's elements must not overlap one another.
-void disjoint(const at::Tensor& x, const char* name) {
-  if (x.is_contiguous()) return;
-  std::vector<std::pair<int64_t, int64_t>> dims;
+using Dims = std::vector<std::pair<int64_t, int64_t>>;     // (stride, size), sizes above 1
+Dims dims_of(const at::Tensor& x) {
+  Dims d;
   for (int64_t i = 0; i < x.dim(); ++i)
-    if (x.size(i) > 1) dims.emplace_back(x.stride(i), x.size(i));
-  std::sort(dims.begin(), dims.end());
+    if (x.size(i) > 1) d.emplace_back(x.stride(i), x.size(i));
+  std::sort(d.begin(), d.end());
+  return d;
+}
+// The last element's offset, and whether every stride steps over all that the smaller
+// ones reach (then no two elements coincide).
+int64_t reach_of(const Dims& d, bool* nested) {
   int64_t reach = 0;
-  for (const auto& [s, n] : dims) {
-    if (s <= reach) refuse("the rows of " + std::string(name) + " overlap");
+  *nested = true;
+  for (const auto& [s, n] : d) {
+    *nested = *nested && s > reach;
     reach += s * (n - 1);
   }
+  return reach;
+}
+
+// Whether two elements of tensors with these nested dimensions, their starts `d` apart,
+// coincide: d is a sum of steps, fewer than the size along each.  What the smaller
+// dimensions can make up for is less than a step, so two counts of steps are possible.
+bool meet(const Dims& dims, size_t n, int64_t d) {
+  if (n == 0) return d == 0;
+  const auto [s, size] = dims[n - 1];
+  const int64_t q = d / s - (d % s < 0);
+  for (int64_t steps : {q, q + 1})
+    if (std::abs(steps) < size && meet(dims, n - 1, d - steps * s)) return true;
+  return false;
+}
+
+// Whether two tensors share memory.  Exact where they are laid out alike, as slices of
+// one buffer are; tensors of different layouts count as sharing where their extents meet.
+bool share(const at::Tensor& a, const at::Tensor& b) {
+  if (a.numel() == 0 || b.numel() == 0) return false;
+  const intptr_t d = static_cast<char*>(b.data_ptr()) - static_cast<char*>(a.data_ptr());
+  if (a.is_contiguous() && b.is_contiguous())
+    return d < static_cast<intptr_t>(a.nbytes()) && d > -static_cast<intptr_t>(b.nbytes());
+  const Dims da = dims_of(a), db = dims_of(b);
+  bool nested, other;
+  const int64_t ea = static_cast<int64_t>(a.element_size()), eb = static_cast<int64_t>(b.element_size());
+  const int64_t ra = (reach_of(da, &nested) + 1) * ea, rb = (reach_of(db, &other) + 1) * eb;
+  if (d >= ra || d <= -rb) return false;
+  return !nested || da != db || ea != eb || d % ea != 0 || meet(da, da.size(), d / ea);
+}
+
+// An output's elements must not overlap one another.
+void disjoint(const at::Tensor& x, const char* name) {
+  bool nested = true;
+  if (!x.is_contiguous()) reach_of(dims_of(x), &nested);
+  if (!nested) refuse("the rows of " + std::string(name) + " overlap");
 }
 
 struct CacheRef {
@@ -265,7 +305,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (x[i].sizes() != at::IntArrayRef(shape)) refuse(std::string(name) + " must be [batch, tokens, heads, head_dim]");
       disjoint(x[i], name);
     }
-    if (x[0].numel() > 0 && x[0].data_ptr() == x[1].data_ptr()) refuse("k and v must not share memory");
+    if (a[8] != Py_None && a[9] != Py_None && share(x[0], x[1])) refuse("k and v must not share memory");
     if (!call("kq_cache_read", c.dev, [&](void* st) {
           return g.cache_read(c.c, static_cast<int32_t*>(table.data_ptr()), B, table.size(1), T,
                               static_cast<int32_t*>(ptr(start)), static_cast<int32_t*>(ptr(lens)), x[0].data_ptr(),
@@ -303,16 +343,13 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const auto os = head_rows(out, at::kBFloat16, c.dev, "out");
     if (out.sizes() != q.sizes()) refuse("out must have the shape of q");
     disjoint(out, "out");
-    if (given && q.numel() > 0) {
-      const intptr_t d = static_cast<char*>(given->data_ptr()) - static_cast<char*>(q.data_ptr());
-      const bool dense = q.is_contiguous() && given->is_contiguous();
-      if (d == 0 || (dense && std::abs(d) < static_cast<intptr_t>(q.nbytes()))) refuse("out and q must not share memory");
-    }
+    if (given && share(q, *given)) refuse("out and q must not share memory");
     const at::Tensor* lse = tensor(a[10], "lse", true);
     if (lse) {
       check_dense(*lse, at::kFloat, c.dev, "lse");
       if (lse->dim() != 3 || lse->size(0) != B || lse->size(1) != H || lse->size(2) != M)
         refuse("lse must be float32 [batch, heads, M]");
+      if (share(*lse, q) || share(*lse, out)) refuse("lse must not share memory with q or out");
     }
     if (B > 0 && M > 0) {
       const size_t need = g.attention_workspace_bytes(B, M, H, c.c->heads, D, max_len);
@@ -320,6 +357,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       at::Tensor own;
       if (ws) {
         check_dense(*ws, at::kByte, c.dev, "workspace");
+        if (share(*ws, q) || share(*ws, out) || (lse && share(*ws, *lse)))
+          refuse("the workspace must not share memory with q, out or lse");
       } else if (need > 0) {
         own = at::empty({static_cast<int64_t>(need)}, q.options().dtype(at::kByte));
         ws = &own;

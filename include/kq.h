@@ -389,7 +389,13 @@ int kq_cache_read(const kq_cache* cache, const int32_t* block_table, int64_t bat
  *   scores, or NULL.
  *   scale: of magnitude below 2^65; the scaled scores, times log2(e), are float32.
  *   max_len: a bound on lens, at most table_pages * page_size and 2^30; the
- *   work is cut by it, so a tight one is faster.
+ *   work is cut by it, so a tight one is faster.  With more than 64 rows (M *
+ *   heads / kv heads) the workspace holds the K and V of max_len positions in
+ *   bf16, batch * kv heads * max_len * head_dim * 4 bytes (max_len rounded up to
+ *   128, head_dim to 16), up to 4 GiB.  Past that, and from 32768 K/V heads on, the
+ *   cache is decoded again for every 32 rows instead (33 x 2048 queries of 32 / 8
+ *   heads over 512 positions: 4.4 against 0.73 ms): give a max_len near the longest sequence, or a call to some of the
+ *   sequences.
  *   workspace: kq_attention_workspace_bytes(...) bytes, 256-byte aligned (NULL
  *   where that is 0); its contents before and after do not matter.  Calls that
  *   overlap on the GPU need their own.

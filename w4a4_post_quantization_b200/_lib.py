@@ -735,7 +735,9 @@ def attention_mxfp4(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, 
     lens[b] positions of each sequence of the cache (causal: the queries are the
     last M of them); heads / cache.heads query heads read one K/V head.  scale (below
     2^65) defaults to head_dim^-0.5, max_len (a bound on lens) to what the block table
-    holds.  lse: an optional float32 [batch, heads, M] output.  A row that sees
+    holds; a tight one is faster, and needs less workspace (with more than 64 query rows of
+    a K/V head 4 bytes for every number of K, up to 4 GiB, past which many rows are many
+    times slower).  lse: an optional float32 [batch, heads, M] output.  A row that sees
     no position gives 0, and -inf in lse; any other row with a NaN or an infinity
     among its queries gives NaN in both.  out, lse and workspace must not share
     memory with q or one another.  Values of blocks below 2^-68 are taken with an

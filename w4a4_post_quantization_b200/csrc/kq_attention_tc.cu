@@ -778,11 +778,6 @@ int launch_tc(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cuda
   return e == cudaSuccess ? KQ_OK : record_cuda_error(e);
 }
 
-template <int kD16>
-int launch_tc_qt(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
-  return launch_tc<kD16>(a, p, batch, dev, st);
-}
-
 }  // namespace
 
 int launch_attention_tc(const AttnArgs& a, const AttnPlan& p, int64_t batch, int dev, cudaStream_t st) {
@@ -792,14 +787,14 @@ int launch_attention_tc(const AttnArgs& a, const AttnPlan& p, int64_t batch, int
       dim3(kDecodeThreads), 0, st, a, const_cast<uint4*>(a.tile_mask), const_cast<uint8_t*>(a.images));
   if (e != cudaSuccess) return record_cuda_error(e);
   switch (a.d16) {
-    case 16: return launch_tc_qt<16>(a, p, batch, dev, st);
-    case 32: return launch_tc_qt<32>(a, p, batch, dev, st);
-    case 48: return launch_tc_qt<48>(a, p, batch, dev, st);
-    case 64: return launch_tc_qt<64>(a, p, batch, dev, st);
-    case 80: return launch_tc_qt<80>(a, p, batch, dev, st);
-    case 96: return launch_tc_qt<96>(a, p, batch, dev, st);
-    case 112: return launch_tc_qt<112>(a, p, batch, dev, st);
-    default: return launch_tc_qt<128>(a, p, batch, dev, st);
+    case 16: return launch_tc<16>(a, p, batch, dev, st);
+    case 32: return launch_tc<32>(a, p, batch, dev, st);
+    case 48: return launch_tc<48>(a, p, batch, dev, st);
+    case 64: return launch_tc<64>(a, p, batch, dev, st);
+    case 80: return launch_tc<80>(a, p, batch, dev, st);
+    case 96: return launch_tc<96>(a, p, batch, dev, st);
+    case 112: return launch_tc<112>(a, p, batch, dev, st);
+    default: return launch_tc<128>(a, p, batch, dev, st);
   }
 }
 

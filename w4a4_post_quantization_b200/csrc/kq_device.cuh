@@ -5,6 +5,7 @@
 
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #if defined(__CUDA_ARCH__) && (__CUDA_ARCH__ < 1000)
@@ -148,6 +149,13 @@ __device__ __forceinline__ f2 sub2(f2 a, f2 b) {
   return d;
 }
 
+// 2^x on the special-function unit; -inf gives 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // 2^y for both halves without the special-function unit, for y >= -126: 2^f of
 // the fraction by the polynomial of degree 4 with the least relative error over
 // [-1/2, 1/2] (2.6e-6, by Remez' exchange), the integer into the exponent.
@@ -165,6 +173,12 @@ __device__ __forceinline__ void ex2_poly(f2 y, float& p0, float& p1) {
   unpack2(q, q0, q1);
   p0 = __uint_as_float(__float_as_uint(q0) + (__float_as_uint(r0) << 23));
   p1 = __uint_as_float(__float_as_uint(q1) + (__float_as_uint(r1) << 23));
+}
+
+// Two floats rounded to bf16, the first in the low half-word.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
 // Two bf16 values (element 2m in the low half-word) widened exactly to f32.

@@ -67,12 +67,6 @@ struct EpArgs {
   int* err;
 };
 
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // The larger of x and lo; NaN stays NaN.  Where an activation has come down to 2^-57 its
 // argument is held: x / (1 + 2^t) with t capped would be 2^-63 of x, however large that
 // is.  (0.7 of 34 us at 8192 x 4608 x 1152 with tanh-GELU; a reciprocal of its own for
@@ -97,8 +91,8 @@ __device__ __forceinline__ f2 over_one_plus_exp2(f2 x, f2 t) {
   float t0, t1, a, b;
   unpack2(t, t0, t1);
   // A NaN does not reach the other half.
-  a = ex2_approx(fminf(t0, 63.0f));
-  b = ex2_approx(fminf(t1, 63.0f));
+  a = ex2(fminf(t0, 63.0f));
+  b = ex2(fminf(t1, 63.0f));
   unpack2(add2(pack2(a, b), pack2(1.0f, 1.0f)), a, b);
   const float r = rcp_approx(a * b);
   return mul2(x, mul2(pack2(r, r), pack2(b, a)));
@@ -138,7 +132,7 @@ __device__ __forceinline__ f2 activate(f2 x) {
     s = fma2(s, t, both(0.254829592f));
     unpack2(mul2(mul2(z, z), both(-1.4426950409f)), z0, z1);
     // Phi(-|v|)
-    const f2 q = mul2(mul2(s, t), mul2(both(0.5f), pack2(ex2_approx(z0), ex2_approx(z1))));
+    const f2 q = mul2(mul2(s, t), mul2(both(0.5f), pack2(ex2(z0), ex2(z1))));
     float q0, q1;
     unpack2(q, q0, q1);
     return mul2(x, pack2(v0 < 0.0f ? q0 : 1.0f - q0, v1 < 0.0f ? q1 : 1.0f - q1));
@@ -187,11 +181,6 @@ __device__ __forceinline__ void finish(uint32_t (&x)[32], const float* bias, con
     for (int c = 0; c < 32; ++c)
       if (col + c < N) x[c] = __float_as_uint(__uint_as_float(x[c]) * bf16_at(own_gate + col + c));
   }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
 template <int kN, bool kBf16, int kAct>
@@ -372,7 +361,7 @@ __global__ void __launch_bounds__(EpGeom<kN>::kThreads, 1)
                 uint32_t ow[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
-                  ow[h] = pack_bf16(__uint_as_float(x[v][e + 2 * h]) + bf16_lo(rw[h]),
+                  ow[h] = bf16x2(__uint_as_float(x[v][e + 2 * h]) + bf16_lo(rw[h]),
                                     __uint_as_float(x[v][e + 2 * h + 1]) + bf16_hi(rw[h]));
                 *at = make_uint4(ow[0], ow[1], ow[2], ow[3]);
               } else {

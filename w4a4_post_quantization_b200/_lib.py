@@ -627,8 +627,8 @@ def gemm_mxfp4_epilogue(qa: torch.Tensor, sa_tiled: torch.Tensor, qb: torch.Tens
     optional, rounded once: gemm_mxfp4_tiled with the rest of a transformer
     layer's product.  bias bf16 [N]; activation "none", "gelu_tanh", "gelu" or
     "silu"; gate bf16 [samples, N] with samples >= ceil(M / tokens_per_sample);
-    residual [M, N] of out's type, and ``out=residual`` adds in place.  K is at
-    most 2^21."""
+    residual [M, N] of out's type, and ``out=residual`` adds in place.  All are
+    contiguous (a chunk of a wider modulation needs a copy).  K is at most 2^21."""
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
     if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:

@@ -91,7 +91,8 @@ __device__ __forceinline__ bool row_sees(const AttnArgs& a, int64_t b, int begin
   return end > begin && cache_row(a.view, b, end - 1, 0) >= 0;
 }
 
-// kNT: groups of 8 query rows.
+// kNT: groups of 8 query rows.  Four with heads of 128 take all 255 registers and spill 268
+// bytes a thread.
 template <int kW, int kNT>
 __global__ void __launch_bounds__(32 * kWarps, kNT == 1 ? 4 : kNT == 2 ? 3 : 2)
     attn_split_kernel(const AttnArgs a) {
@@ -522,7 +523,8 @@ AttnPlan make_plan(int64_t batch, int64_t kv_heads, int64_t rows, int64_t max_le
     p.row_groups = static_cast<int>((rows + 8 * p.nt - 1) / (8 * p.nt));
     constexpr int64_t kStep = kTile * kWarps;
     // About twelve CTAs for each SM, of at least 512 positions (8 x 8 heads, 18 to
-    // 33 thousand positions: six 96 us, eight 87, twelve 85, twenty-four 90).
+    // 33 thousand positions: six 96 us, eight 87, twelve 85, twenty-four 90; with the
+    // tests for rows that are no numbers twelve takes 87).
     const int64_t units = batch * kv_heads * p.row_groups;
     const int64_t want = std::max<int64_t>(1, 12 * kSms / units);
     const int64_t chunk = std::max<int64_t>(512, (max_len + want - 1) / want);

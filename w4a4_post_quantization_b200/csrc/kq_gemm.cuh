@@ -127,7 +127,8 @@ __device__ __forceinline__ void pair_tile_origin(const PairTiles& a, int t, int&
 
 // One thread of each CTA: the stages' loads.  Every load of the pair counts
 // its bytes on rank 0's stage barrier; none uses cluster multicast.  False if
-// a bounded wait gave up.
+// a bounded wait gave up; the copies still counted then were issued before that wait,
+// of 10 ms and more, and have landed.
 template <int kN, int kStagesP>
 __device__ __forceinline__ bool pair_produce(uint8_t* base, uint64_t* full, uint64_t* empty,
                                              const CUtensorMap* amap, const CUtensorMap* bmap,

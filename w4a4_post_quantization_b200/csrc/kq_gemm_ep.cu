@@ -38,7 +38,8 @@ constexpr int kBoxBytes = kBoxRows * 128;
 constexpr int kEpStaging = 65536;             // the epilogue warps' boxes
 
 // Registers a thread: wide tiles have 20 warps, launched with 96, of which the
-// epilogue's take 104 and the others keep 64.
+// epilogue's take 104 and the others keep 64.  Some spill: 4 and 16 bytes with GELU and
+// tanh-GELU, and the narrow bf16 tiles, with 168, 8 to 124 bytes.
 constexpr int kEpRegs = 104, kRestRegs = 64;
 
 template <int kN>

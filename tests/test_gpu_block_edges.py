@@ -163,3 +163,35 @@ print("ok")
 def test_the_first_call_of_a_process_can_be_captured(what):
     run = subprocess.run([sys.executable, "-c", FIRST, what], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and run.stdout.strip() == "ok", run.stderr[-2000:]
+
+
+def test_float32_rows_read_into_strided_outputs():
+    B, T, H, D = 2, 37, 3, 40
+    cache = kq.cache_alloc(6, 16, H, D, device=DEV)
+    table = i32([[0, 1, 2], [5, 4, 3]])
+    k, v = rows((B, T, H, D), 1), rows((B, T, H, D), 2)
+    kq.cache_write(cache, table, k, v)
+    fused = torch.full((B, H, T + 2, 2 * D), 7.0, device=DEV)
+    a, b = (fused[:, :, 1:-1, i * D:(i + 1) * D].transpose(1, 2) for i in range(2))
+    gk, gv = kq.cache_read(cache, table, i32([T, 20]), T, out_dtype=torch.float32, k=a, v=b)
+    want = round_trip(k)
+    want[1, 20:] = 0
+    assert gk.data_ptr() == a.data_ptr() and np.array_equal(a.double().cpu().numpy(), want)
+    want = round_trip(v)
+    want[1, 20:] = 0
+    assert np.array_equal(b.double().cpu().numpy(), want)
+    assert (fused[:, :, 0] == 7).all() and (fused[:, :, -1] == 7).all()
+
+
+@pytest.mark.parametrize("M", [1, 30, 100])
+@pytest.mark.parametrize("max_len", [1, 15, 17, 129])
+def test_short_bounds_and_a_query_shared_by_the_batch(M, max_len):
+    B, H, D, L = 3, 4, 56, 140
+    cache, table, k, v = make_cache(B, L, 2, D, 16, seed=M)
+    kd, vd = fill(cache, table, k, v, [L] * B)
+    q = queries(1, M, H, D, 4).expand(B, M, H, D)
+    lens = [L, 16, 0]
+    lse = torch.empty((B, H, M), device=DEV)
+    out = kq.attention_mxfp4(q.to(DEV)[:1].expand(B, M, H, D), cache, table, i32(lens), causal=True, max_len=max_len, lse=lse)
+    assert kq.device_status() == 0
+    check(out, lse, q.double().numpy(), kd, vd, [min(n, max_len) for n in lens], True)
